@@ -98,7 +98,9 @@ EXPORTED = ["attn_block_fwd", "attn_block_fwd_workspace_size", "attn_merge", "ri
             "ba_sync_status", "ba_debug_wait_timeout", "ba_strerror", "attn_block_fwd_noalloc",
             "attn_block_bwd", "attn_block_bwd_workspace_size", "ring_attn_bwd", "ring_attn_bwd_workspace_size",
             "ulysses_all_to_all", "ulysses_attn_fwd", "ulysses_attn_fwd_workspace_size",
-            "attn_decode_fwd", "attn_decode_workspace_size", "ba_pair_schedule"]
+            "attn_decode_fwd", "attn_decode_workspace_size", "ba_pair_schedule",
+            "attn_window_fwd", "attn_window_fwd_workspace_size", "attn_window_bwd",
+            "attn_window_bwd_workspace_size"]
 
 
 def load(path: str | None = None):
@@ -160,6 +162,15 @@ def load(path: str | None = None):
     lib.attn_decode_workspace_size.argtypes = [i, i, i, i, i]
     lib.attn_decode_fwd.restype = i
     lib.attn_decode_fwd.argtypes = [T, T, T, i, i, i, i, i, vp, i, f, vp, i, vp, vp, sz, vp]
+    lib.attn_window_fwd_workspace_size.restype = sz
+    lib.attn_window_fwd_workspace_size.argtypes = []
+    lib.attn_window_fwd.restype = i
+    lib.attn_window_fwd.argtypes = [T, T, T, i, i, i, i, i, i, i, i64, i, i, vp, i64, f, vp, i, vp, vp, sz, vp]
+    lib.attn_window_bwd_workspace_size.restype = sz
+    lib.attn_window_bwd_workspace_size.argtypes = [i, i, i, i, i, i, i64, i, i]
+    lib.attn_window_bwd.restype = i
+    lib.attn_window_bwd.argtypes = [T, T, T, T, T, vp, i, i, i, i, i, i, i, i64, i, i, vp, i64, f, vp, vp, vp, i,
+                                    vp, sz, vp]
     _lib = lib
     return lib
 
@@ -460,6 +471,121 @@ def ulysses_attn_fwd(q_tok, k_tok, v_tok, *, key_padding_mask=None, attn_mask=No
                               _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream))
     _check("ulysses_attn_fwd", rc)
     return out, lse
+
+
+def _like(ref, **tensors):
+    """Every tensor on ref's device, and that device the current one (launches and torch's streams go there)."""
+    if ref.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {ref.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def _kv_heads(q, k, v):
+    """Checks k, v (B, Hkv, L, d) against q (B, Hq, .., d) and returns (Hkv, L)."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("expected q (B, Hq, L, d) and k, v (B, Hkv, L, d) of one shape")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share a dtype")
+    if k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise ValueError(f"k, v of shape {tuple(k.shape)} do not match q of shape {tuple(q.shape)}")
+    Hkv = k.shape[1]
+    if Hkv == 0 or q.shape[1] % Hkv:
+        raise ValueError(f"{q.shape[1]} query heads are not a multiple of {Hkv} key heads")
+    return Hkv, k.shape[2]
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor from the memory of the stream that the call runs on (so that nothing
+    still pending on another stream uses the memory, and its reuse waits for this call)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out_pair(q, out, out_dtype, lse, stream):
+    """The outputs of an attention call on q: allocated, or the caller's checked."""
+    if out is None:
+        out = _empty(q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out does not have out_dtype")
+    if lse is None:
+        lse = _empty(q.shape[:3], torch.float32, q.device, stream)
+    _check_out(out, lse, q.shape)
+    _like(q, out=out, lse=lse)
+    return out, lse
+
+
+def _scratch(need, workspace, device, stream):
+    """(pointer, bytes, tensor) of a workspace: the caller's or a new one (the tensor is kept until the launch)."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _empty((need,), torch.uint8, device, stream)
+    elif not workspace.is_contiguous() or workspace.dtype != torch.uint8 or workspace.device != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace
+
+
+def _c_int(name, x, lo):
+    x = int(x)
+    if not lo <= x < 1 << 31:
+        raise ValueError(f"{name} = {x} is not in [{lo}, 2^31)")
+    return x
+
+
+def attn_window_fwd(q, k, v, *, window, sinks=0, q_off=0, key_padding_mask=None, scale=None, out=None, out_dtype=None,
+                    lse=None, workspace=None, stream=None):
+    """Causal attention with a sliding window and `sinks` first keys that stay visible:
+    q (B, Hq, Lq, d) at positions q_off + i against k, v (B, Hkv, Lk, d) at positions
+    0 .. Lk - 1, Hkv dividing Hq; see include/blockattn.h.  Returns (out, lse)."""
+    lib = load()
+    Hkv, Lk = _kv_heads(q, k, v)
+    B, Hq, Lq, d = q.shape
+    window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
+    tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
+    _like(q, k=k, v=v, key_padding_mask=key_padding_mask)
+    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    kpm, kpm_ld = _mask(key_padding_mask, B, Lk, "key_padding_mask")
+    ws, ws_bytes, keep = _scratch(lib.attn_window_fwd_workspace_size(), workspace, q.device, stream)
+    rc = lib.attn_window_fwd(tq, tk, tv, B, Hq, Hkv, Lq, Lk, d, _dtype_code(q.dtype), q_off, window, sinks, kpm, kpm_ld,
+                             0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
+                             ws, ws_bytes, _stream(stream))
+    _check("attn_window_fwd", rc)
+    return out, lse
+
+
+def attn_window_bwd(q, k, v, out, dout, lse, *, window, sinks=0, q_off=0, key_padding_mask=None, scale=None, dq=None,
+                    dk=None, dv=None, grad_dtype=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of attn_window_fwd from its out and lse; of q's dtype
+    unless grad_dtype (or the given buffers) say float32; see include/blockattn.h."""
+    lib = load()
+    Hkv, Lk = _kv_heads(q, k, v)
+    B, Hq, Lq, d = q.shape
+    window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
+    tensors = _tensor(q), _tensor(k), _tensor(v), _tensor(out), _tensor(dout)
+    _check_bwd_inputs(q, out, dout, lse)
+    _like(q, k=k, v=v, out=out, dout=dout, lse=lse, key_padding_mask=key_padding_mask, dq=dq, dk=dk, dv=dv)
+    given = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype)
+    grad_dtype = given if grad_dtype is None else grad_dtype
+    grads = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            t = _empty(like.shape, grad_dtype, q.device, stream)
+        elif t.dtype != grad_dtype or not t.is_contiguous() or t.shape != like.shape:
+            raise ValueError(f"{name} must be a contiguous {grad_dtype} CUDA tensor of shape {tuple(like.shape)}")
+        grads.append(t)
+    dq, dk, dv = grads
+    kpm, kpm_ld = _mask(key_padding_mask, B, Lk, "key_padding_mask")
+    need = lib.attn_window_bwd_workspace_size(B, Hq, Hkv, Lq, Lk, d, q_off, window, sinks)
+    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
+    rc = lib.attn_window_bwd(*tensors, _ptr(lse), B, Hq, Hkv, Lq, Lk, d, _dtype_code(q.dtype), q_off, window, sinks,
+                             kpm, kpm_ld, 0.0 if scale is None else float(scale), _ptr(dq), _ptr(dk), _ptr(dv),
+                             _dtype_code(grad_dtype), ws, ws_bytes, _stream(stream))
+    _check("attn_window_bwd", rc)
+    return dq, dk, dv
 
 
 def attn_decode_fwd(q, k_cache, v_cache, *, lengths=None, num_splits=0, scale=None, out=None, out_dtype=None,

@@ -1651,6 +1651,231 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok, in
 }
 
 // ---------------------------------------------------------------------------
+// Sliding window with sinks
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// The window and the sinks as far as they matter for queries up to position
+// last - 1: a window that covers every position makes the sinks ordinary keys.
+struct WindowSpec {
+    int window, sinks;
+};
+
+WindowSpec window_spec(int window, int sinks, long long last, int Lk) {
+    WindowSpec w;
+    w.window = window < last ? window : (int)(last > 1 ? last : 1);
+    w.sinks = w.window >= last ? 0 : (sinks < Lk ? sinks : Lk);
+    return w;
+}
+
+// How the queries of the key tiles that hold sinks are cut: chunks of about one
+// walk of an ordinary key tile (window + 128 rows), at most about 32 in all, so that
+// no item outlasts the others and the partials stay small.
+struct SinkParts {
+    int tiles, parts, rows;
+};
+
+SinkParts sink_parts(const WindowSpec &w, int Lq, int tile_rows) {
+    SinkParts p{0, 1, Lq};
+    const int tiles = ceil_div(w.sinks, tile_rows);
+    if (tiles == 0 || Lq == 0) return p;
+    long long rows = (long long)w.window + TILE, least = ((long long)Lq * tiles + 31) / 32;
+    if (rows < least) rows = least;
+    rows = (rows + TILE - 1) / TILE * TILE;
+    if (rows >= Lq) return p;   // one chunk: the tiles are items like the others
+    p.tiles = tiles;
+    p.rows = (int)rows;
+    p.parts = ceil_div(Lq, (int)rows);
+    return p;
+}
+
+int check_window(int B, int Hq, int Hkv, int Lq, int Lk, int dtype, int64_t q_off, int window, int sinks,
+                 const uint8_t *kpm, int64_t kpm_ld) {
+    if (B < 0 || Hq < 0 || Hkv < 0 || Lq < 0 || Lk < 0 || q_off < 0 || window < 1 || sinks < 0 || !valid_dtype(dtype))
+        return BA_ERR_ARG;
+    if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return BA_ERR_SHAPE;
+    if (q_off + Lq > 0x7fffffffLL - 2 * TILE || Lk > 0x7fffffffLL - 2 * TILE) return BA_ERR_SHAPE;
+    if ((long long)B * Hq * (ceil_div(Lq, 64) + 1) > 0x7fffffffLL) return BA_ERR_SHAPE;   // work items are ints
+    if (kpm && kpm_ld < Lk) return BA_ERR_ARG;
+    return BA_OK;
+}
+
+int window_heads_per_group(int B, int Hq, int Hkv, long long keys, int d, int dtype) {
+    return heads_per_group(B, Hkv, keys, d, dtype) * (Hq / Hkv);
+}
+
+}  // namespace
+
+size_t attn_window_fwd_workspace_size(void) { return sched_bytes(1); }
+
+int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hkv, int Lq, int Lk, int d, int dtype,
+                    int64_t q_off, int window, int sinks, const uint8_t *key_padding_mask, int64_t kpm_ld, float scale,
+                    void *out, int out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                    ba_stream_t stream) {
+    int rc = check_window(B, Hq, Hkv, Lq, Lk, dtype, q_off, window, sinks, key_padding_mask, kpm_ld);
+    if (rc) return rc;
+    const bool rows_exist = (long long)B * Hq * Lq > 0;
+    if (rows_exist && (check_tensor(q) || !out || !lse)) return BA_ERR_ARG;
+    if (rows_exist && Lk > 0 && (check_tensor(k) || check_tensor(v))) return BA_ERR_ARG;
+    if (!valid_d(d)) return BA_ERR_SHAPE;
+    if (out_dtype != BA_F32 && out_dtype != dtype) return BA_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(out) % 16) return BA_ERR_ARG;   // rows are stored in 16-byte vectors
+    if (!rows_exist) return BA_OK;
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    q = fix_unit_strides(q, B, Hq, Lq, d);
+    k = fix_unit_strides(k, B, Hkv, Lk, d);
+    v = fix_unit_strides(v, B, Hkv, Lk, d);
+
+    AttnArgs a;
+    std::memset(&a, 0, sizeof a);
+    Geom &g = a.g;
+    const WindowSpec w = window_spec(window, sinks, q_off + Lq, Lk);
+    g.B = B;
+    g.H = Hq;
+    g.d = d;
+    g.Lq = Lq;
+    g.Lk = Lk;
+    g.q_off = q_off;
+    g.nqt_pc = g.n_qtiles = ceil_div(Lq, TILE);
+    g.nkt_pc = g.n_ktiles = ceil_div(Lk, TILE);
+    g.heads_per_group = window_heads_per_group(B, Hq, Hkv, Lk, d, dtype);
+    g.n_items = g.n_qtiles * B * Hq;
+    g.causal = 1;
+    g.kpm = key_padding_mask;
+    g.kpm_ld = kpm_ld;
+    g.window = w.window;
+    g.sinks = w.sinks;
+    g.kv_group = Hq / Hkv;
+    a.q = q.ptr;
+    a.k = k.ptr;
+    a.v = v.ptr;
+    a.qsB = q.sB; a.qsH = q.sH; a.qsT = q.sT;
+    a.ksB = k.sB; a.ksH = k.sH; a.ksT = k.sT;
+    a.vsB = v.sB; a.vsH = v.sH; a.vsT = v.sT;
+    a.dtype = dtype;
+    const float sc = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)d));
+    a.scale_log2 = sc * LOG2E;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse;
+    a.rows = Lq;
+    a.err = g_err_ptr[dev];
+    a.wait_limit_ns = kWaitLimitNs;
+    if (!tc_supported(dtype, d) || Lk == 0 || !tma_ok(q, B, Hq) || !tma_ok(k, B, Hkv) || !tma_ok(v, B, Hkv))
+        return launch_attn_simt(a, stream);
+    if ((rc = get_encoder())) return rc;
+    // With no more items than SMs every CTA takes one: dealt round-robin, without the
+    // counter and the launch that clears it.
+    Scratch ws;
+    if ((long long)n_pairs(g) * B * Hq > g_num_sms[dev]) {
+        if ((rc = ws.acquire(workspace, workspace_bytes, sched_bytes(1), stream))) return rc;
+        a.sched = static_cast<unsigned *>(ws.ptr);
+        if ((rc = zero_sched(ws.ptr, 1, stream))) return rc;
+    }
+    TmaMaps m;
+    std::memset(&m, 0, sizeof m);
+    a.tma_out = a.out_dtype == BA_BF16;
+    if ((rc = encode_map(&m.q, q.ptr, d, Lq, Hq, B, q.sT, q.sH, q.sB))) return rc;
+    if ((rc = encode_map(&m.k, k.ptr, d, Lk, Hkv, B, k.sT, k.sH, k.sB))) return rc;
+    if ((rc = encode_map(&m.v, v.ptr, d, Lk, Hkv, B, v.sT, v.sH, v.sB))) return rc;
+    if (a.tma_out && encode_map(&m.o, out, d, Lq, Hq, B, d, (long long)Lq * d, (long long)Hq * Lq * d, 32)) a.tma_out = 0;
+    return launch_attn_tc(a, m, g_num_sms[dev], stream);
+}
+
+// Item counters, D, then the partials of the key tiles that hold sinks.
+size_t attn_window_bwd_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d, int64_t q_off, int window,
+                                      int sinks) {
+    if (B < 0 || Hq < 0 || Hkv < 0 || Lq < 0 || Lk < 0 || d < 1 || q_off < 0 || window < 1 || sinks < 0) return 0;
+    const SinkParts p = sink_parts(window_spec(window, sinks, q_off + Lq, Lk), Lq, TILE);
+    return 256 + align256((size_t)4 * B * Hq * Lq) + align256((size_t)8 * B * Hkv * p.tiles * p.parts * TILE * d);
+}
+
+int attn_window_bwd(ba_tensor q, ba_tensor k, ba_tensor v, ba_tensor out, ba_tensor dout, const float *lse, int B,
+                    int Hq, int Hkv, int Lq, int Lk, int d, int dtype, int64_t q_off, int window, int sinks,
+                    const uint8_t *key_padding_mask, int64_t kpm_ld, float scale, void *dq, void *dk, void *dv,
+                    int grad_dtype, void *workspace, size_t workspace_bytes, ba_stream_t stream) {
+    int rc = check_window(B, Hq, Hkv, Lq, Lk, dtype, q_off, window, sinks, key_padding_mask, kpm_ld);
+    if (rc) return rc;
+    if (!valid_d(d)) return BA_ERR_SHAPE;
+    if (grad_dtype != BA_F32 && grad_dtype != dtype) return BA_ERR_ARG;
+    const bool qrows = (long long)B * Hq * Lq > 0, krows = (long long)B * Hkv * Lk > 0;
+    if (qrows && (check_tensor(q) || check_tensor(out) || check_tensor(dout) || !lse || !dq)) return BA_ERR_ARG;
+    if (krows && (check_tensor(k) || check_tensor(v) || !dk || !dv)) return BA_ERR_ARG;
+    const size_t ge = elem_size(grad_dtype);
+    if (!qrows || !krows) {   // one side is empty: the other's gradients are zero
+        if (qrows && cudaMemsetAsync(dq, 0, (size_t)B * Hq * Lq * d * ge, stream) != cudaSuccess) return BA_ERR_CUDA;
+        if (krows && (cudaMemsetAsync(dk, 0, (size_t)B * Hkv * Lk * d * ge, stream) != cudaSuccess ||
+                      cudaMemsetAsync(dv, 0, (size_t)B * Hkv * Lk * d * ge, stream) != cudaSuccess))
+            return BA_ERR_CUDA;
+        return BA_OK;
+    }
+    if (B * (long long)Hq > 65535) return BA_ERR_SHAPE;
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    Scratch ws;
+    const size_t need = attn_window_bwd_workspace_size(B, Hq, Hkv, Lq, Lk, d, q_off, window, sinks);
+    if ((rc = ws.acquire(workspace, workspace_bytes, need, stream))) return rc;
+    ba::BwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.B = B;
+    a.H = Hq;
+    a.d = d;
+    a.dtype = dtype;
+    a.Lq = Lq;
+    a.Lk = Lk;
+    a.q_off = q_off;
+    a.causal = 1;
+    a.kpm = key_padding_mask;
+    a.kpm_ld = kpm_ld;
+    q = fix_unit_strides(q, B, Hq, Lq, d);
+    out = fix_unit_strides(out, B, Hq, Lq, d);
+    dout = fix_unit_strides(dout, B, Hq, Lq, d);
+    k = fix_unit_strides(k, B, Hkv, Lk, d);
+    v = fix_unit_strides(v, B, Hkv, Lk, d);
+    a.q = tref(q);
+    a.out = tref(out);
+    a.dout = tref(dout);
+    a.k = tref(k);
+    a.v = tref(v);
+    a.lse = lse;
+    a.sched = static_cast<unsigned *>(ws.ptr);
+    a.D = reinterpret_cast<float *>(static_cast<uint8_t *>(ws.ptr) + 256);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws.ptr) + 256 + align256((size_t)4 * B * Hq * Lq));
+    a.heads_per_group = window_heads_per_group(B, Hq, Hkv, Lq > Lk ? Lq : Lk, d, dtype);
+    a.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)d));
+    a.dq = static_cast<float *>(dq);
+    a.dk = static_cast<float *>(dk);
+    a.dv = static_cast<float *>(dv);
+    a.grad_bf16 = grad_dtype == BA_BF16;
+    a.Hkv = Hkv;
+    a.kv_group = Hq / Hkv;
+    const WindowSpec w = window_spec(window, sinks, q_off + Lq, Lk);
+    a.window = w.window;
+    a.sinks = w.sinks;
+    a.err = g_err_ptr[dev];
+    a.wait_limit_ns = kWaitLimitNs;
+    auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };   // 16-byte stores
+    const bool tc = ba::bwd_tc_supported(dtype, d) && tma_ok(q, B, Hq) && tma_ok(k, B, Hkv) && tma_ok(v, B, Hkv) &&
+                    tma_ok(dout, B, Hq) && al16(dq) && al16(dk) && al16(dv);
+    const SinkParts p = sink_parts(w, Lq, tc ? TILE : 64);
+    a.n_sink_tiles = p.tiles;
+    a.n_sink_parts = p.parts;
+    a.sink_rows = p.rows;
+    if (!tc) return ba::launch_attn_window_bwd(a, g_num_sms[dev], stream);
+    if ((rc = get_encoder())) return rc;
+    ba::BwdMaps m;
+    if ((rc = encode_map(&m.q, q.ptr, d, Lq, Hq, B, q.sT, q.sH, q.sB))) return rc;
+    if ((rc = encode_map(&m.dout, dout.ptr, d, Lq, Hq, B, dout.sT, dout.sH, dout.sB))) return rc;
+    if ((rc = encode_map(&m.k, k.ptr, d, Lk, Hkv, B, k.sT, k.sH, k.sB))) return rc;
+    if ((rc = encode_map(&m.v, v.ptr, d, Lk, Hkv, B, v.sT, v.sH, v.sB))) return rc;
+    return ba::launch_attn_window_bwd_tc(a, m, g_num_sms[dev], stream);
+}
+
+// ---------------------------------------------------------------------------
 // Decode with a split KV cache
 // ---------------------------------------------------------------------------
 
@@ -1733,6 +1958,244 @@ int attn_decode_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int H, int S, 
     a.out_dtype = out_dtype;
     a.lse = lse;
     return ba::launch_decode(a, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens of grouped heads: windowed cache, 4-bit cache
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Most keys that a sequence can see, and the splits of that range.
+long long most_keys(int S, int window, int sinks) {
+    if (window == 0) return S;
+    const long long n = (long long)window + sinks;
+    return n < S ? n : S;
+}
+
+size_t decode_group_bytes(long long rows, int n_splits, int d) {
+    if (n_splits <= 1) return 0;
+    return align256((size_t)rows * n_splits * d * 4) + align256((size_t)rows * n_splits * 8);
+}
+
+size_t decode_group_workspace(int B, int Hq, int Hkv, int S, int d, int window, int sinks, bool kv4) {
+    if (B < 0 || Hq < 0 || Hkv < 1 || S < 0 || d < 1 || window < 0 || sinks < 0 || Hq % Hkv) return 0;
+    const int dev = current_device();
+    const int sms = dev >= 0 && g_num_sms[dev] > 0 ? g_num_sms[dev] : 152;
+    const long long n = most_keys(S, window, sinks);
+    int splits = ba::decode_group_splits(B, Hkv, Hq / Hkv, n, kv4, sms);
+    const int other = ba::decode_group_splits(B, Hkv, Hq / Hkv, n, kv4, 152);   // before the device is known
+    if (other > splits) splits = other;
+    return decode_group_bytes((long long)B * Hq, splits, d);
+}
+
+int check_decode_group(int B, int Hq, int Hkv, int S, int dtype, int window, int sinks, int out_dtype, float scale) {
+    if (B < 0 || Hq < 0 || Hkv < 0 || S < 0 || window < 0 || sinks < 0 || !valid_dtype(dtype) || scale != scale)
+        return BA_ERR_ARG;
+    if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return BA_ERR_SHAPE;
+    if (out_dtype != BA_F32 && out_dtype != dtype) return BA_ERR_ARG;
+    if ((long long)B * Hkv > 65535 || (long long)B * Hq > 0x7fffffffLL / 128 || S > 0x7fffffff - 256)
+        return BA_ERR_SHAPE;
+    return BA_OK;
+}
+
+// Fills in what both caches share and launches.
+int run_decode_group(ba::DecodeGroupArgs &a, const ba_tensor &q, int B, int Hq, int Hkv, int S, int d, int dtype,
+                     const int32_t *lengths, int window, int sinks, void *out, int out_dtype, float *lse, void *workspace,
+                     size_t workspace_bytes, int dev, cudaStream_t stream) {
+    a.B = B;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.S = S;
+    a.d = d;
+    a.dtype = dtype;
+    a.q = q.ptr;
+    a.qsB = q.sB;
+    a.qsH = q.sH;
+    a.lengths = lengths;
+    a.window = window;
+    a.sinks = window > 0 ? sinks : 0;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse;
+    const long long n = most_keys(S, window, sinks);
+    const bool kv4 = a.k_scales != nullptr;
+    a.n_splits = ba::decode_group_splits(B, Hkv, a.G, n, kv4, g_num_sms[dev]);
+    a.split_len = n > 0 ? (int)((n + a.n_splits - 1) / a.n_splits) : 1;
+    a.split_len = (a.split_len + 63) / 64 * 64;   // whole tiles for every warp
+    Scratch ws;
+    const int rc = ws.acquire(workspace, workspace_bytes, decode_group_bytes((long long)B * Hq, a.n_splits, d), stream);
+    if (rc) return rc;
+    a.part_o = static_cast<float *>(ws.ptr);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws.ptr) +
+                                           align256((size_t)B * Hq * a.n_splits * d * 4));
+    return ba::launch_decode_group(a, stream);
+}
+
+bool kv4_ok(const ba_kv4 &c, int B, int H) {
+    auto al = [](const void *p, unsigned n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
+    if (!al(c.k_codes, 16) || !al(c.v_codes, 16) || !al(c.k_scales, 8) || !al(c.v_scales, 8)) return false;
+    if (c.codes_sT % 16 || c.scales_sT % 8) return false;
+    if (H > 1 && (c.codes_sH % 16 || c.scales_sH % 8)) return false;
+    if (B > 1 && (c.codes_sB % 16 || c.scales_sB % 8)) return false;
+    return c.k_exp >= -100 && c.k_exp <= 100 && c.v_exp >= -100 && c.v_exp <= 100;
+}
+
+void kv4_args(ba::Kv4Args &a, const ba_kv4 &c) {
+    void *codes[2] = {c.k_codes, c.v_codes}, *scales[2] = {c.k_scales, c.v_scales};
+    for (int i = 0; i < 2; ++i) {
+        a.codes[i] = codes[i];
+        a.scales[i] = scales[i];
+        a.csB[i] = c.codes_sB;
+        a.csH[i] = c.codes_sH;
+        a.csT[i] = c.codes_sT;
+        a.ssB[i] = c.scales_sB;
+        a.ssH[i] = c.scales_sH;
+        a.ssT[i] = c.scales_sT;
+    }
+    a.exp[0] = c.k_exp;
+    a.exp[1] = c.v_exp;
+}
+
+}  // namespace
+
+size_t attn_window_decode_workspace_size(int B, int Hq, int Hkv, int S, int d, int window, int sinks) {
+    return window < 1 ? 0 : decode_group_workspace(B, Hq, Hkv, S, d, window, sinks, false);
+}
+
+int attn_window_decode_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hkv, int S, int d, int dtype,
+                           const int32_t *lengths, int window, int sinks, float scale, void *out, int out_dtype,
+                           float *lse, void *workspace, size_t workspace_bytes, ba_stream_t stream) {
+    if (window < 1) return BA_ERR_ARG;
+    int rc = check_decode_group(B, Hq, Hkv, S, dtype, window, sinks, out_dtype, scale);
+    if (rc) return rc;
+    if (!valid_d(d)) return BA_ERR_SHAPE;
+    if ((long long)B * Hq == 0) return BA_OK;
+    if (check_tensor(q) || !out || !lse || (S > 0 && (check_tensor(k) || check_tensor(v)))) return BA_ERR_ARG;
+    const size_t eb = elem_size(dtype);
+    q = fix_unit_strides(q, B, Hq, 1, d);
+    if (Hq <= 1) q.sH = d;
+    k = fix_unit_strides(k, B, Hkv, S, d);
+    v = fix_unit_strides(v, B, Hkv, S, d);
+    if (!rows16(q.ptr, B > 1 ? q.sB : 0, Hq > 1 ? q.sH : 0, d, eb) ||
+        (S > 0 && (!rows16(k.ptr, B > 1 ? k.sB : 0, Hkv > 1 ? k.sH : 0, S > 1 ? k.sT : 0, eb) ||
+                   !rows16(v.ptr, B > 1 ? v.sB : 0, Hkv > 1 ? v.sH : 0, S > 1 ? v.sT : 0, eb))))
+        return BA_ERR_ARG;   // the kernels read 16-byte vectors of every row
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    ba::DecodeGroupArgs a;
+    std::memset(&a, 0, sizeof a);
+    const long long e = (long long)eb;
+    a.k = k.ptr;
+    a.ksB = k.sB * e;
+    a.ksH = k.sH * e;
+    a.ksT = k.sT * e;
+    a.v = v.ptr;
+    a.vsB = v.sB * e;
+    a.vsH = v.sH * e;
+    a.vsT = v.sT * e;
+    a.scale_log2 = (scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)d))) * LOG2E;
+    a.out_mul = 1.f;
+    return run_decode_group(a, q, B, Hq, Hkv, S, d, dtype, lengths, window, sinks, out, out_dtype, lse, workspace,
+                            workspace_bytes, dev, stream);
+}
+
+size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int S, int d, int window, int sinks) {
+    return decode_group_workspace(B, Hq, Hkv, S, d, window, sinks, true);
+}
+
+int attn_decode_kv4_fwd(ba_tensor q, ba_kv4 cache, int B, int Hq, int Hkv, int S, int d, int dtype,
+                        const int32_t *lengths, int window, int sinks, float scale, void *out, int out_dtype, float *lse,
+                        void *workspace, size_t workspace_bytes, ba_stream_t stream) {
+    int rc = check_decode_group(B, Hq, Hkv, S, dtype, window, sinks, out_dtype, scale);
+    if (rc) return rc;
+    if (dtype != BA_BF16) return BA_ERR_UNSUPPORTED;
+    if (d != 64 && d != 128) return BA_ERR_SHAPE;
+    if ((long long)B * Hq == 0) return BA_OK;
+    if (check_tensor(q) || !out || !lse || (S > 0 && !kv4_ok(cache, B, Hkv))) return BA_ERR_ARG;
+    q = fix_unit_strides(q, B, Hq, 1, d);
+    if (!rows16(q.ptr, B > 1 ? q.sB : 0, Hq > 1 ? q.sH : 0, d, 2)) return BA_ERR_ARG;
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    ba::DecodeGroupArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.k = cache.k_codes;
+    a.v = cache.v_codes;
+    a.ksB = a.vsB = cache.codes_sB;
+    a.ksH = a.vsH = cache.codes_sH;
+    a.ksT = a.vsT = cache.codes_sT;
+    a.k_scales = S > 0 ? cache.k_scales : q.ptr;   // (marks the cache's kind; an empty cache is not read)
+    a.v_scales = cache.v_scales;
+    a.kcB = a.vcB = cache.scales_sB;
+    a.kcH = a.vcH = cache.scales_sH;
+    a.kcT = a.vcT = cache.scales_sT;
+    a.scale_log2 = std::ldexp((scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)d))) * LOG2E, cache.k_exp);
+    a.out_mul = std::ldexp(1.f, cache.v_exp);
+    return run_decode_group(a, q, B, Hq, Hkv, S, d, dtype, lengths, window, sinks, out, out_dtype, lse, workspace,
+                            workspace_bytes, dev, stream);
+}
+
+int kv4_append(ba_tensor k, ba_tensor v, ba_kv4 cache, int B, int H, int T, int S, int d, int dtype,
+               const int32_t *start, const int32_t *counts, ba_stream_t stream) {
+    if (B < 0 || H < 0 || T < 0 || S < 0 || !valid_dtype(dtype)) return BA_ERR_ARG;
+    if (d != 64 && d != 128) return BA_ERR_SHAPE;
+    if ((long long)B * H * T == 0 || S == 0) return BA_OK;
+    if (!kv4_ok(cache, B, H)) return BA_ERR_ARG;
+    const size_t eb = elem_size(dtype);
+    ba::Kv4Args a;
+    std::memset(&a, 0, sizeof a);
+    const ba_tensor x[2] = {k, v};
+    for (int i = 0; i < 2; ++i) {
+        if (check_tensor(x[i]) || !rows16(x[i].ptr, B > 1 ? x[i].sB : 0, H > 1 ? x[i].sH : 0, T > 1 ? x[i].sT : 0, eb))
+            return BA_ERR_ARG;
+        a.x[i] = x[i].ptr;
+        a.xsB[i] = x[i].sB;
+        a.xsH[i] = x[i].sH;
+        a.xsT[i] = x[i].sT;
+    }
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    const int rc = device_setup(dev);
+    if (rc) return rc;
+    a.B = B;
+    a.H = H;
+    a.T = T;
+    a.S = S;
+    a.d = d;
+    a.dtype = dtype;
+    a.start = start;
+    a.counts = counts;
+    kv4_args(a, cache);
+    return ba::launch_kv4_append(a, g_num_sms[dev], stream);
+}
+
+int kv4_read(ba_kv4 cache, int B, int H, int S, int d, int first, int T, int dtype, void *k, void *v,
+             ba_stream_t stream) {
+    if (B < 0 || H < 0 || T < 0 || S < 0 || first < 0 || !valid_dtype(dtype) || (long long)first + T > S)
+        return BA_ERR_ARG;
+    if (d != 64 && d != 128) return BA_ERR_SHAPE;
+    if ((long long)B * H * T == 0) return BA_OK;
+    if (!kv4_ok(cache, B, H) || !k || !v) return BA_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(k) % 16 || reinterpret_cast<uintptr_t>(v) % 16) return BA_ERR_ARG;
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    const int rc = device_setup(dev);
+    if (rc) return rc;
+    ba::Kv4Args a;
+    std::memset(&a, 0, sizeof a);
+    a.B = B;
+    a.H = H;
+    a.T = T;
+    a.S = S;
+    a.d = d;
+    a.dtype = dtype;
+    a.first = first;
+    a.y[0] = k;
+    a.y[1] = v;
+    kv4_args(a, cache);
+    return ba::launch_kv4_read(a, g_num_sms[dev], stream);
 }
 
 // Same work as attn_block_fwd, with the tile-class map in the library's fixed

@@ -136,6 +136,7 @@ __device__ __forceinline__ void bwd_item(const BwdArgs &a, int w, int n_side, bo
 struct PWalk {
     int step, span;
     long long row, row_end, dpos;
+    long long lo, hi;   // window: the rows of the later steps
     bool open;
 };
 
@@ -210,6 +211,124 @@ __device__ __forceinline__ bool pwalk_next(const BwdArgs &a, const BTile &own, b
         w.open = pwalk_span(a, own, own_is_key, w);
     }
     return false;
+}
+
+// ---------------------------------------------------------------------------
+// Sliding window with sinks (template parameter W of the kernels)
+// ---------------------------------------------------------------------------
+//
+// A key tile without sinks is seen by the queries at positions [k_first, k_last +
+// window), a key tile that holds sinks by every later query: as one item it would
+// outlast all others (its walk is the sequence, theirs the window), so its queries
+// are cut into n_sink_parts chunks of about a window, each an item of its own that
+// writes an fp32 partial; sink_sum_kernel adds the partials of a row in their
+// order.  (Where one chunk would hold every query, n_sink_tiles is 0 and the tile
+// is an item like the others.)  Query heads h share key head h / kv_group: a key tile's walk takes its
+// query rows once for each head of the group, so dK and dV need no atomics.
+
+// dK/dV item w -> key tile, b * Hkv + head, chunk of the queries (-1: all of the tile's window).
+__device__ __forceinline__ void window_kv_item(const BwdArgs &a, int w, int n_side, int &tile, int &bh, int &part) {
+    const int BH = a.B * a.Hkv, sink = BH * a.n_sink_tiles * a.n_sink_parts;
+    if (w < sink) {
+        part = w % a.n_sink_parts;
+        tile = w / a.n_sink_parts % a.n_sink_tiles;
+        bh = w / a.n_sink_parts / a.n_sink_tiles;
+        return;
+    }
+    part = -1;
+    w -= sink;
+    const int own = n_side - a.n_sink_tiles, G = a.heads_per_group > a.kv_group ? a.heads_per_group / a.kv_group : 1;
+    const int per_group = G * own, grp = w / per_group, rem = w % per_group;
+    const int g_heads = BH - grp * G < G ? BH - grp * G : G;
+    tile = a.n_sink_tiles + rem / g_heads;
+    bh = grp * G + rem % g_heads;
+}
+
+__device__ __forceinline__ int window_kv_items(const BwdArgs &a, int n_side) {
+    return a.B * a.Hkv * (n_side - a.n_sink_tiles + a.n_sink_tiles * a.n_sink_parts);
+}
+
+// The walk of a window item.  Keys own: step = head of the group, the same rows at
+// each.  Queries own: the sink keys before the window, then the window.
+__device__ __forceinline__ void wwalk_begin(const BwdArgs &a, const BTile &own, bool own_is_key, int part, PWalk &w) {
+    w.step = 0;
+    if (own_is_key) {
+        long long lo = own.pos0 - a.q_off, hi = own.pos0 + own.len - 1 + a.window - a.q_off;
+        if (part >= 0) {
+            const long long p0 = (long long)part * a.sink_rows;
+            lo = lo > p0 ? lo : p0;
+            hi = p0 + a.sink_rows;
+        } else if (own.pos0 < a.sinks) {
+            hi = a.Lq;   // sinks taken whole: one chunk covers every query
+        }
+        w.lo = lo > 0 ? lo : 0;
+        w.hi = hi < a.Lq ? hi : a.Lq;
+        w.span = a.kv_group;   // steps
+        w.dpos = a.q_off;
+        w.row = w.lo;
+        w.row_end = w.hi;
+    } else {
+        const long long end = own.pos0 + own.len < a.Lk ? own.pos0 + own.len : a.Lk;
+        long long lo = own.pos0 - (long long)TILE * (((long long)a.window - 1 + TILE - 1) / TILE);
+        if (lo <= a.sinks) lo = 0;
+        w.lo = lo;
+        w.hi = end;
+        w.span = lo > 0 ? 2 : 1;
+        w.dpos = 0;
+        w.row = 0;
+        w.row_end = lo > 0 ? (a.sinks < end ? a.sinks : end) : end;
+    }
+}
+
+__device__ __forceinline__ bool wwalk_next(PWalk &w, BTile &p) {
+    while (w.row >= w.row_end) {
+        if (++w.step >= w.span) return false;
+        w.row = w.lo;
+        w.row_end = w.hi;
+        if (w.lo >= w.hi) return false;
+    }
+    p.row0 = w.row;
+    p.len = (int)min((long long)TILE, w.row_end - w.row);
+    p.pos0 = w.row + w.dpos;
+    p.chunk = 0;
+    w.row += TILE;
+    return true;
+}
+
+template <bool W>
+__device__ __forceinline__ void walk_begin(const BwdArgs &a, const BTile &own, bool own_is_key, int part, PWalk &w) {
+    if constexpr (W)
+        wwalk_begin(a, own, own_is_key, part, w);
+    else
+        pwalk_begin(a, own, own_is_key, w);
+}
+
+template <bool W>
+__device__ __forceinline__ bool walk_next(const BwdArgs &a, const BTile &own, bool own_is_key, PWalk &w, BTile &p) {
+    if constexpr (W)
+        return wwalk_next(w, p);
+    else
+        return pwalk_next(a, own, own_is_key, w, p);
+}
+
+__device__ __forceinline__ uint32_t low_bits(long long n) {   // the n lowest bits
+    return n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u);
+}
+
+// Key kp against the queries at positions q0 + i, i < 32, of which the first n exist.
+__device__ __forceinline__ uint32_t window_bits_queries(const BwdArgs &a, long long q0, int n, long long kp) {
+    const long long hi = kp < a.sinks ? (long long)n : min((long long)n, kp + a.window - q0);
+    return low_bits(hi) & ~low_bits(kp - q0);
+}
+
+// The query at position qp against the keys k0 + i, i < 32, of which the first n exist.
+__device__ __noinline__ uint32_t window_bits_keys(const BwdArgs &a, int b, long long qp, long long k0, int n) {
+    uint32_t m = low_bits(min((long long)n, qp - k0 + 1));
+    m &= ~low_bits(qp - a.window + 1 - k0) | low_bits(a.sinks - k0);
+    if (a.kpm)
+        for (int i = 0; i < 32 && i < n; ++i)
+            if (a.kpm[b * a.kpm_ld + k0 + i]) m &= ~(1u << i);
+    return m;
 }
 
 __device__ __forceinline__ bool bexcluded(const BwdArgs &a, int b, long long qp, long long kp) {
@@ -335,11 +454,46 @@ __device__ __forceinline__ void store_acc_row(uint32_t taddr, float *dst, float 
     }
 }
 
+// The same to a gradient of either type (bf16: rounded once, here).
+template <int D>
+__device__ __forceinline__ void store_grad_row(uint32_t taddr, void *dst, long long at, float mul, bool bf16, bool valid,
+                                               int c_begin = 0, int c_end = D / 32) {
+    if (!bf16) {
+        store_acc_row<D>(taddr, static_cast<float *>(dst) + at, mul, false, valid, c_begin, c_end);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        if (c < c_begin || c >= c_end) continue;
+        uint32_t r[32];
+        tmem_ld32(taddr + c * 32, r);
+        tmem_wait_ld();
+        if (!valid) continue;
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(dst) + at + c * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                p[k] = pack_bf16(__uint_as_float(r[8 * i + 2 * k]) * mul, __uint_as_float(r[8 * i + 2 * k + 1]) * mul);
+            o[i] = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+    }
+}
+
+// n zeros from element `at` of a gradient of either type.
+__device__ __forceinline__ void zero_grad(void *dst, long long at, int n, bool bf16) {
+    if (bf16)
+        for (int c = 0; c < n; ++c) static_cast<__nv_bfloat16 *>(dst)[at + c] = __float2bfloat16_rn(0.f);
+    else
+        for (int c = 0; c < n; ++c) static_cast<float *>(dst)[at + c] = 0.f;
+}
+
 // ---------------------------------------------------------------------------
 // dK, dV
 // ---------------------------------------------------------------------------
 
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(384, 1)
     bwd_dkdv_tc_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo) {
@@ -360,7 +514,7 @@ __global__ void __launch_bounds__(384, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long q_rows = a.ring ? a.T : a.Lq;
-    const int n_side = n_tiles_side(a, false), n_items = n_side * a.B * a.H;
+    const int n_side = n_tiles_side(a, false), n_items = W ? window_kv_items(a, n_side) : n_side * a.B * a.H;
     const uint64_t lim = a.wait_limit_ns;
     const uint32_t tmem = bwd_prologue<D>(bars, misc, base + C::MISC_OFF, 32, &tq, &tk, &tv, &tdo);
 
@@ -386,9 +540,12 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) mbar_arrive(bar(C::B_ITEMF + sl));
                 break;
             }
-            int ktile, bh;
-            bwd_item(a, w, n_side, false, ktile, bh);
-            const int b = bh / a.H, h = bh % a.H;
+            int ktile, bh, part = -1;
+            if constexpr (W)
+                window_kv_item(a, w, n_side, ktile, bh, part);
+            else
+                bwd_item(a, w, n_side, false, ktile, bh);
+            const int b = bh / (W ? a.Hkv : a.H), h = bh % (W ? a.Hkv : a.H);
             const BTile kt = btile(a, ktile, false);
             if (lane == 0) misc[4 + sl] = (uint32_t)w;
             __syncwarp();
@@ -404,9 +561,9 @@ __global__ void __launch_bounds__(384, 1)
             }
             ++loads;
             PWalk pw;
-            pwalk_begin(a, kt, true, pw);
+            walk_begin<W>(a, kt, true, part, pw);
             BTile pt;
-            while (ok && pwalk_next(a, kt, true, pw, pt)) {
+            while (ok && walk_next<W>(a, kt, true, pw, pt)) {
                 const int st = fills % C::NST;
                 const uint32_t use = fills / C::NST;
                 if (use > 0 && !warp_wait(bar(C::B_EMPTY + st), (use - 1) & 1, abort, a.err, lim)) {
@@ -414,12 +571,13 @@ __global__ void __launch_bounds__(384, 1)
                     break;
                 }
                 float *lse2 = vec(st), *dd = lse2 + TILE;
+                const int hq = W ? h * a.kv_group + pw.step : h;   // query head of this tile
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = lane * 4 + i;
                     float L = -INFINITY, Dv = 0.f;
                     if (c < pt.len) {
-                        const long long row = (long long)bh * q_rows + pt.row0 + c;
+                        const long long row = (W ? (long long)b * a.H + hq : (long long)bh) * q_rows + pt.row0 + c;
                         L = a.lse[row];
                         Dv = a.D[row];
                     }
@@ -430,8 +588,8 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(C::B_FULL + st), 2 * C::TILE_BYTES);
-                    tma_tile<D>(stage(st), &tq, pt.row0, h, b, bar(C::B_FULL + st));
-                    tma_tile<D>(stage(st) + C::TILE_BYTES, &tdo, pt.row0, h, b, bar(C::B_FULL + st));
+                    tma_tile<D>(stage(st), &tq, pt.row0, hq, b, bar(C::B_FULL + st));
+                    tma_tile<D>(stage(st) + C::TILE_BYTES, &tdo, pt.row0, hq, b, bar(C::B_FULL + st));
                 } else {
                     mbar_arrive(bar(C::B_FULL + st));
                 }
@@ -511,17 +669,20 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_ITEME + sl));
             if (w == 0xffffffffu) break;
-            int ktile, bh;
-            bwd_item(a, (int)w, n_side, false, ktile, bh);
+            int ktile, bh, part = -1;
+            if constexpr (W)
+                window_kv_item(a, (int)w, n_side, ktile, bh, part);
+            else
+                bwd_item(a, (int)w, n_side, false, ktile, bh);
             const BTile kt = btile(a, ktile, false);
             if (!warp_wait(bar(C::B_RES), it & 1, abort, a.err, lim)) {
                 ok = false;
                 break;
             }
             PWalk pw;
-            pwalk_begin(a, kt, true, pw);
+            walk_begin<W>(a, kt, true, part, pw);
             BTile pt;
-            bool have = pwalk_next(a, kt, true, pw, pt);
+            bool have = walk_next<W>(a, kt, true, pw, pt);
             if (!have) {
                 // no query sees this key tile: the accumulators are not touched
                 mma_commit_one(bar(C::B_RESE));
@@ -535,7 +696,7 @@ __global__ void __launch_bounds__(384, 1)
             bool first = true;
             while (have) {
                 const int st = t % C::NST, stn = (t + 1) % C::NST;
-                const bool more = pwalk_next(a, kt, true, pw, pt);
+                const bool more = walk_next<W>(a, kt, true, pw, pt);
                 if (!more) mma_commit_one(bar(C::B_RESE));   // the item's last score products are issued
                 if (first && it > 0 && !(ok = warp_wait(bar(C::B_ACCE), (it - 1) & 1, abort, a.err, lim))) break;
                 if (!(ok = grads(st, 0, t, first))) break;
@@ -577,21 +738,26 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_ITEME + sl));
             if (w == 0xffffffffu) break;
-            int ktile, bh;
-            bwd_item(a, (int)w, n_side, false, ktile, bh);
-            const int b = bh / a.H;
+            int ktile, bh, part = -1;
+            if constexpr (W)
+                window_kv_item(a, (int)w, n_side, ktile, bh, part);
+            else
+                bwd_item(a, (int)w, n_side, false, ktile, bh);
+            const int b = bh / (W ? a.Hkv : a.H);
             const BTile kt = btile(a, ktile, false);
             const bool jvalid = j < kt.len;
             const long long kp = kt.pos0 + j;
+            const bool jseen = W ? jvalid && !(a.kpm && a.kpm[b * a.kpm_ld + kp]) : jvalid;
             uint32_t n_done = 0;   // query tiles of this item (the same for every lane)
             PWalk pw;
-            pwalk_begin(a, kt, true, pw);
+            walk_begin<W>(a, kt, true, part, pw);
             BTile pt;
-            while (ok && pwalk_next(a, kt, true, pw, pt)) {
+            while (ok && walk_next<W>(a, kt, true, pw, pt)) {
                 const int st = t % C::NST;
                 const uint32_t s_nlse = smem_u32(vec(st)), s_dd = s_nlse + TILE * 4;   // -LSE log2 units, D
                 const bool full = kt.len == TILE && pt.len == TILE && !a.kpm && !a.am &&
-                                  (!a.causal || kt.pos0 + TILE - 1 <= pt.pos0);
+                                  (!a.causal || kt.pos0 + TILE - 1 <= pt.pos0) &&
+                                  (!W || pt.pos0 + TILE - 1 < kt.pos0 + a.window || kt.pos0 + TILE <= a.sinks);
 #pragma unroll 1
                 for (int c = 2 * grp; c < 2 * grp + 2; ++c) {
                     const int hh = c >> 1;   // half of the tile: queries [64 hh, 64 hh + 64)
@@ -608,6 +774,7 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_wait_ld();
                     const uint32_t keep =
                         full ? 0xffffffffu
+                        : W  ? (jseen ? window_bits_queries(a, pt.pos0 + c * 32, pt.len - c * 32, kp) : 0u)
                              : keep_bits_queries(a, b, pt.pos0 + c * 32, pt.len - c * 32, kp, jvalid);
                     uint32_t pp[16], pd[16];
 #pragma unroll
@@ -623,6 +790,7 @@ __global__ void __launch_bounds__(384, 1)
                             p = (keep >> i) & 1u ? p : 0.f;   // columns past the partner tile are never kept
                             pv[e] = p;
                             dv[e] = p * (__uint_as_float(rd[i]) - ddv[e]);
+                            if (W) dv[e] = (keep >> i) & 1u ? dv[e] : 0.f;   // a padded V row may hold anything
                         }
                         pp[q4 * 2] = pack_bf16(pv[0], pv[1]);
                         pp[q4 * 2 + 1] = pack_bf16(pv[2], pv[3]);
@@ -653,7 +821,19 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             const long long row = ((long long)bh * (a.ring ? a.T : a.Lk) + kt.row0 + j) * D;
             // group 0 writes the dV rows, group 1 the dK rows
-            if (n_done > 0) {   // the same for every lane: the TMEM loads below stay warp-collective
+            if constexpr (W) {
+                const bool to_part = part >= 0;
+                void *dst = to_part ? a.part : (grp == 0 ? (void *)a.dv : (void *)a.dk);
+                const long long at =
+                    to_part ? (((((long long)bh * a.n_sink_tiles + ktile) * a.n_sink_parts + part) * 2 + grp) * TILE + j) * D
+                            : row;
+                const bool b16 = !to_part && a.grad_bf16;
+                if (n_done > 0)
+                    store_grad_row<D>(tmem + lane_addr + (grp == 0 ? C::ACC0_COL : C::ACC1_COL), dst, at,
+                                      grp == 0 ? 1.f : a.scale, b16, jvalid);
+                else if (jvalid)
+                    zero_grad(dst, at, D, b16);
+            } else if (n_done > 0) {   // the same for every lane: the TMEM loads below stay warp-collective
                 if (grp == 0)
                     store_acc_row<D>(tmem + lane_addr + C::ACC0_COL, a.dv + row, 1.f, a.accumulate != 0, jvalid);
                 else
@@ -679,7 +859,7 @@ __global__ void __launch_bounds__(384, 1)
 // dQ
 // ---------------------------------------------------------------------------
 
-template <int D>
+template <int D, bool W>
 __global__ void __launch_bounds__(384, 1)
     bwd_dq_tc_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo) {
@@ -736,9 +916,9 @@ __global__ void __launch_bounds__(384, 1)
                 tma_tile<D>(sDO, &tdo, qt.row0, h, b, bar(C::B_RES));
                 ++loads;
                 PWalk pw;
-                pwalk_begin(a, qt, false, pw);
+                walk_begin<W>(a, qt, false, -1, pw);
                 BTile pt;
-                while (pwalk_next(a, qt, false, pw, pt)) {
+                while (walk_next<W>(a, qt, false, pw, pt)) {
                     const int st = fills % C::NST;
                     const uint32_t use = fills / C::NST;
                     if (use > 0 && !mbar_wait(bar(C::B_EMPTY + st), (use - 1) & 1, abort, a.err, lim)) {
@@ -746,8 +926,8 @@ __global__ void __launch_bounds__(384, 1)
                         break;
                     }
                     mbar_arrive_expect_tx(bar(C::B_FULL + st), 2 * C::TILE_BYTES);
-                    tma_tile<D>(stage(st), &tk, pt.row0, h, b, bar(C::B_FULL + st));
-                    tma_tile<D>(stage(st) + C::TILE_BYTES, &tv, pt.row0, h, b, bar(C::B_FULL + st));
+                    tma_tile<D>(stage(st), &tk, pt.row0, W ? h / a.kv_group : h, b, bar(C::B_FULL + st));
+                    tma_tile<D>(stage(st) + C::TILE_BYTES, &tv, pt.row0, W ? h / a.kv_group : h, b, bar(C::B_FULL + st));
                     ++fills;
                 }
                 if (!ok) break;
@@ -820,9 +1000,9 @@ __global__ void __launch_bounds__(384, 1)
                 break;
             }
             PWalk pw;
-            pwalk_begin(a, qt, false, pw);
+            walk_begin<W>(a, qt, false, -1, pw);
             BTile pt;
-            bool have = pwalk_next(a, qt, false, pw, pt);
+            bool have = walk_next<W>(a, qt, false, pw, pt);
             if (!have) {
                 mma_commit_one(bar(C::B_RESE));
                 if (it > 0 && !(ok = warp_wait(bar(C::B_ACCE), (it - 1) & 1, abort, a.err, lim))) break;
@@ -835,7 +1015,7 @@ __global__ void __launch_bounds__(384, 1)
             bool first = true;
             while (have) {
                 const int st = t % C::NST, stn = (t + 1) % C::NST;
-                const bool more = pwalk_next(a, qt, false, pw, pt);
+                const bool more = walk_next<W>(a, qt, false, pw, pt);
                 if (!more) mma_commit_one(bar(C::B_RESE));   // the item's last score products are issued
                 if (first && it > 0 && !(ok = warp_wait(bar(C::B_ACCE), (it - 1) & 1, abort, a.err, lim))) break;
                 if (!(ok = grads(st, 0, t, first))) break;
@@ -892,11 +1072,12 @@ __global__ void __launch_bounds__(384, 1)
             }
             uint32_t n_done = 0;   // key tiles of this item (the same for every lane)
             PWalk pw;
-            pwalk_begin(a, qt, false, pw);
+            walk_begin<W>(a, qt, false, -1, pw);
             BTile pt;
-            while (ok && pwalk_next(a, qt, false, pw, pt)) {
+            while (ok && walk_next<W>(a, qt, false, pw, pt)) {
                 const bool full = qt.len == TILE && pt.len == TILE && !a.kpm && !a.am &&
-                                  (!a.causal || pt.pos0 + TILE - 1 <= qt.pos0);
+                                  (!a.causal || pt.pos0 + TILE - 1 <= qt.pos0) &&
+                                  (!W || qt.pos0 + TILE - 1 < pt.pos0 + a.window || pt.pos0 + TILE <= a.sinks);
 #pragma unroll 1
                 for (int c = 2 * grp; c < 2 * grp + 2; ++c) {
                     const int hh = c >> 1;   // half of the tile: keys [64 hh, 64 hh + 64)
@@ -906,13 +1087,31 @@ __global__ void __launch_bounds__(384, 1)
                             break;
                         }
                         tc_fence_after();
+                        if constexpr (W) {
+                            // a padded key's K row may hold anything: zeroed (its scores are
+                            // formed) before dQ += dS K of this half is released
+                            if (a.kpm && i < C::HALF) {
+                                const int r = hh * C::HALF + i;
+                                if (r >= pt.len || a.kpm[b * a.kpm_ld + pt.pos0 + r]) {
+                                    const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                                    for (int u = 0; u < 8 * C::NBOX; ++u)
+                                        st_shared_v4(stage(t % C::NST) + (u >> 3) * C::BOX_BYTES + r * 128 + (u & 7) * 16,
+                                                     zero);
+                                    fence_proxy_async_shared();
+                                }
+                            }
+                            __syncwarp();
+                        }
                     }
                     uint32_t rs[32], rd[32];
                     tmem_ld32(tmem + lane_addr + C::S_COL + c * 32, rs);
                     tmem_ld32(tmem + lane_addr + C::DP_COL + c * 32, rd);
                     tmem_wait_ld();
                     const uint32_t keep =
-                        full ? 0xffffffffu : keep_bits_keys(a, b, qp, ivalid, pt.pos0 + c * 32, pt.len - c * 32);
+                        full ? 0xffffffffu
+                        : W  ? (ivalid ? window_bits_keys(a, b, qp, pt.pos0 + c * 32, pt.len - c * 32) : 0u)
+                             : keep_bits_keys(a, b, qp, ivalid, pt.pos0 + c * 32, pt.len - c * 32);
                     uint32_t pd[16];
 #pragma unroll
                     for (int k2 = 0; k2 < 16; ++k2) {
@@ -923,6 +1122,7 @@ __global__ void __launch_bounds__(384, 1)
                             float p = fast_exp2(fmaf(__uint_as_float(rs[k]), sl2, nlse2));
                             p = (keep >> k) & 1u ? p : 0.f;
                             dv[e] = p * (__uint_as_float(rd[k]) - Dv);
+                            if (W) dv[e] = (keep >> k) & 1u ? dv[e] : 0.f;
                         }
                         pd[k2] = pack_bf16(dv[0], dv[1]);
                     }
@@ -948,7 +1148,13 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             const long long row = ((long long)bh * q_rows + qt.row0 + i) * D;
             // group g writes columns [g D/2, g D/2 + D/2) of the dQ rows
-            if (n_done > 0)   // uniform: the TMEM loads stay warp-collective
+            if constexpr (W) {
+                if (n_done > 0)
+                    store_grad_row<D>(tmem + lane_addr + C::ACC0_COL, a.dq, row, a.scale, a.grad_bf16 != 0, ivalid,
+                                      grp * (D / 64), grp * (D / 64) + D / 64);
+                else if (ivalid)
+                    zero_grad(a.dq, row + grp * (D / 2), D / 2, a.grad_bf16 != 0);
+            } else if (n_done > 0)   // uniform: the TMEM loads stay warp-collective
                 store_acc_row<D>(tmem + lane_addr + C::ACC0_COL, a.dq + row, a.scale, a.accumulate != 0, ivalid,
                                  grp * (D / 64), grp * (D / 64) + D / 64);
             else if (ivalid && !a.accumulate)
@@ -966,13 +1172,13 @@ __global__ void __launch_bounds__(384, 1)
                      : "memory");
 }
 
-template <int D>
+template <int D, bool W>
 int launch_bwd_tc_d(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s) {
     using C = BCfg<D>;
     static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
-    if (cudaFuncSetAttribute(bwd_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(bwd_dkdv_tc_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(bwd_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+        cudaFuncSetAttribute(bwd_dq_tc_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
             cudaSuccess)
         return BA_ERR_CUDA;
     // CTAs claim (own tile, b, h) items from a zeroed counter, heaviest first.  Short
@@ -984,12 +1190,15 @@ int launch_bwd_tc_d(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_
     const long long n_kt = a.ring ? (long long)a.NC * ((a.CL + TILE - 1) / TILE) : (a.Lk + TILE - 1) / TILE;
     const long long n_qt = a.ring ? (long long)a.NC * ((a.CL + TILE - 1) / TILE) : (a.Lq + TILE - 1) / TILE;
     if (n_kt * BH > 0x7fffffffLL || n_qt * BH > 0x7fffffffLL) return BA_ERR_SHAPE;
-    const bool persistent = n_kt < 256 && n_qt < 256;
+    const bool persistent = W || (n_kt < 256 && n_qt < 256);   // a window's walks are short
     const long long cap = persistent ? num_sms : 0x7fffffffLL;
-    const int g_kv = (int)(n_kt * BH < cap ? n_kt * BH : cap);
+    const long long kv_items =
+        W ? (long long)a.B * a.Hkv * (n_kt - a.n_sink_tiles + (long long)a.n_sink_tiles * a.n_sink_parts) : n_kt * BH;
+    if (kv_items > 0x7fffffffLL) return BA_ERR_SHAPE;
+    const int g_kv = (int)(kv_items < cap ? kv_items : cap);
     const int g_q = (int)(n_qt * BH < cap ? n_qt * BH : cap);
-    if (g_kv > 0) bwd_dkdv_tc_kernel<D><<<g_kv, 384, C::SMEM_BYTES, s>>>(a, m.q, m.k, m.v, m.dout);
-    if (g_q > 0) bwd_dq_tc_kernel<D><<<g_q, 384, C::SMEM_BYTES, s>>>(a, m.q, m.k, m.v, m.dout);
+    if (g_kv > 0) bwd_dkdv_tc_kernel<D, W><<<g_kv, 384, C::SMEM_BYTES, s>>>(a, m.q, m.k, m.v, m.dout);
+    if (g_q > 0) bwd_dq_tc_kernel<D, W><<<g_q, 384, C::SMEM_BYTES, s>>>(a, m.q, m.k, m.v, m.dout);
     return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
 }
 
@@ -1002,9 +1211,24 @@ int launch_attn_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStre
     if ((long long)a.B * a.H == 0) return BA_OK;
     int rc = launch_bwd_pre(a, num_sms, s);
     if (rc) return rc;
-    if (a.d == 128) return launch_bwd_tc_d<128>(a, m, num_sms, s);
-    if (a.d == 64) return launch_bwd_tc_d<64>(a, m, num_sms, s);
+    if (a.d == 128) return launch_bwd_tc_d<128, false>(a, m, num_sms, s);
+    if (a.d == 64) return launch_bwd_tc_d<64, false>(a, m, num_sms, s);
     return BA_ERR_SHAPE;
+}
+
+// The window form: the same kernels over the window's walks, then the sum of the
+// sink tiles' partials.
+int launch_attn_window_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s) {
+    if ((long long)a.B * a.H == 0) return BA_OK;
+    int rc = launch_bwd_pre(a, num_sms, s);
+    if (rc) return rc;
+    if (a.d == 128)
+        rc = launch_bwd_tc_d<128, true>(a, m, num_sms, s);
+    else if (a.d == 64)
+        rc = launch_bwd_tc_d<64, true>(a, m, num_sms, s);
+    else
+        rc = BA_ERR_SHAPE;
+    return rc ? rc : launch_sink_sum(a, TILE, num_sms, s);
 }
 
 }  // namespace ba

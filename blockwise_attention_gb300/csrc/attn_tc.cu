@@ -54,7 +54,7 @@ namespace {
 // ST: the layout has the output staging region (instantiations that store
 // full tiles by TMA); without it the shared-memory carve-out stays smaller,
 // which leaves more L1 for the long-walk kernel's spill slots.
-template <int D, bool ST>
+template <int D, int ST>
 struct Cfg {
     static constexpr int NBOX = D / 64;            // 64-column boxes per tile
     static constexpr int BOX_BYTES = TILE * 128;   // 128 rows x 128 bytes
@@ -163,6 +163,7 @@ struct Keep4 {
     uint32_t m[4];
 };
 
+template <int S>
 __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, bool row_valid, long long kpos0,
                                          int klen) {
     Keep4 r;
@@ -174,6 +175,13 @@ __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, b
             const long long lim = qpos - kpos0 - 32 * c;   // key 32 c + i lies in the future when i > lim
             if (lim < 0) m = 0u;
             else if (lim < 31) m &= (2u << lim) - 1u;
+        }
+        if constexpr (S == WALK_WINDOW) {
+            const long long lo = qpos - g.window + 1 - kpos0 - 32 * c;   // first key of the window
+            const long long ns = g.sinks - kpos0 - 32 * c;               // sink keys of this word
+            const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : ~((1u << lo) - 1u));
+            const uint32_t snk = ns >= 32 ? 0xffffffffu : (ns > 0 ? (1u << ns) - 1u : 0u);
+            m &= win | snk;
         }
         r.m[c] = m;
     }
@@ -200,7 +208,7 @@ __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, b
 // Kernel
 // ----------------------------------------------------------------------------
 
-template <int D, bool S, bool PF>
+template <int D, int S, bool PF>
 __global__ void __launch_bounds__(320, 1)
     attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -300,6 +308,7 @@ __global__ void __launch_bounds__(320, 1)
                 }
                 const QPair p = work_pair<S>(g, w);
                 const bool has1 = p.q1.len > 0;
+                const int kvh = S == WALK_WINDOW ? p.q0.h / g.kv_group : p.q0.h;   // head of the keys
                 misc[4 + sl] = (uint32_t)w;
                 misc[2 + sl] = (uint32_t)pair_count<S>(g, p) | (has1 ? 0x80000000u : 0u);
                 mbar_arrive(bar(C::B_ITEMFULL + sl));
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(320, 1)
                         mbar_arrive_expect_tx(bar(C::B_VFULL + st), C::TILE_BYTES);
                         for (int bx = 0; bx < C::NBOX; ++bx)
                             tma_load_rows<S>(sV + st * C::TILE_BYTES + bx * C::BOX_BYTES, &tv, g, bx * 64, prev_row,
-                                          p.q0.h, p.q0.b, bar(C::B_VFULL + st));
+                                          kvh, p.q0.b, bar(C::B_VFULL + st));
                         ++vfill;
                     }
                     if (more) {
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(320, 1)
                         mbar_arrive_expect_tx(bar(C::B_KFULL + st), C::TILE_BYTES);
                         for (int bx = 0; bx < C::NBOX; ++bx)
                             tma_load_rows<S>(sK + st * C::TILE_BYTES + bx * C::BOX_BYTES, &tk, g, bx * 64, kt.row0,
-                                          p.q0.h, p.q0.b, bar(C::B_KFULL + st));
+                                          kvh, p.q0.b, bar(C::B_KFULL + st));
                         ++kfill;
                     }
                     if (!more) break;
@@ -583,9 +592,35 @@ __global__ void __launch_bounds__(320, 1)
                 // FULL tiles need no predicate; PARTIAL ones, and tiles EMPTY for this
                 // group's rows (seen only by the other tile of the pair), are masked.
                 const bool masked = kt.cls != BA_TILE_FULL || kt.len < TILE;
+                if constexpr (S == WALK_WINDOW) {
+                    // Padded keys get probability 0, which a product with an infinite or NaN
+                    // value would not keep: their V rows (and those of a short tile's
+                    // remaining box rows, which belong to other keys) are zeroed in shared
+                    // memory before P_0, and with it PV_0 and PV_1, is released.
+                    if (g.kpm && x == 0) {
+                        const uint32_t tv_ = tcnt - 1;   // tiles so far = V stages filled so far
+                        const uint32_t st = tv_ % C::VS;
+                        const bool hide = row >= kt.len || g.kpm[qt.b * g.kpm_ld + kt.pos0 + row];
+                        if (__any_sync(0xffffffffu, hide)) {
+                            if (!warp_wait(bar(C::B_VFULL + st), (tv_ / C::VS) & 1, abort, a.err, lim)) {
+                                ok = false;
+                                break;
+                            }
+                            if (hide) {
+                                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                                for (int u = 0; u < 8 * C::NBOX; ++u)
+                                    st_shared_v4(sV + st * C::TILE_BYTES + (u >> 3) * C::BOX_BYTES + row * 128 + (u & 7) * 16,
+                                                 zero);
+                                fence_proxy_async_shared();
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
                 Keep4 keep;
                 if constexpr (PF) {
-                    if (masked) keep = keep_bits4(g, qt.b, qpos, row < qt.len, kt.pos0, kt.len);
+                    if (masked) keep = keep_bits4<S>(g, qt.b, qpos, row < qt.len, kt.pos0, kt.len);
                 }
                 if (!warp_wait(bar(C::B_SFULL + x), sx & 1, abort, a.err, lim)) {
                     ok = false;
@@ -746,7 +781,7 @@ __global__ void __launch_bounds__(320, 1)
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (S)
+                        if constexpr (S == WALK_STRIPED)
                             tma_store_5d(&to, ost, bx * 64, qt.rank, (int)qt.pos0 + 32 * quad, qt.h, qt.b);
                         else
                             tma_store_4d(&to, ost, bx * 64, qt.row0 + 32 * quad, qt.h, qt.b);
@@ -790,7 +825,7 @@ __global__ void __launch_bounds__(320, 1)
     }
 }
 
-template <int D, bool S, bool PF>
+template <int D, int S, bool PF>
 int launch_dpf(const AttnArgs &a, const TmaMaps &m, int num_sms, cudaStream_t s) {
     using C = Cfg<D, PF>;
     static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
@@ -807,9 +842,9 @@ int launch_dpf(const AttnArgs &a, const TmaMaps &m, int num_sms, cudaStream_t s)
 // ranks (a diagonal in every block), or when a head has fewer than 256 key
 // tiles (T < 32K: the causal diagonal tiles are one in about 17 of a walk
 // or more).
-template <int D, bool S>
+template <int D, int S>
 int launch_d(const AttnArgs &a, const TmaMaps &m, int num_sms, cudaStream_t s) {
-    if constexpr (S) {
+    if constexpr (S != WALK_PLAIN) {
         return launch_dpf<D, S, true>(a, m, num_sms, s);
     } else {
         const bool pf = a.g.kpm != nullptr || a.g.am != nullptr || a.g.n_ktiles < 256;
@@ -829,13 +864,18 @@ int launch_attn_tc(const AttnArgs &a, const TmaMaps &m, int num_sms, cudaStream_
     ap.g.n_items = n_pairs(a.g) * a.g.B * a.g.H;
     ap.g.tail_levels = pair_tail_levels(a.g, num_sms);
     if (ap.g.n_items == 0 || a.g.n_qtiles == 0) return BA_OK;
-    if (a.g.striped) {
-        if (a.g.d == 128) return launch_d<128, true>(ap, m, num_sms, s);
-        if (a.g.d == 64) return launch_d<64, true>(ap, m, num_sms, s);
+    if (a.g.window > 0) {
+        if (a.g.d == 128) return launch_d<128, WALK_WINDOW>(ap, m, num_sms, s);
+        if (a.g.d == 64) return launch_d<64, WALK_WINDOW>(ap, m, num_sms, s);
         return BA_ERR_SHAPE;
     }
-    if (a.g.d == 128) return launch_d<128, false>(ap, m, num_sms, s);
-    if (a.g.d == 64) return launch_d<64, false>(ap, m, num_sms, s);
+    if (a.g.striped) {
+        if (a.g.d == 128) return launch_d<128, WALK_STRIPED>(ap, m, num_sms, s);
+        if (a.g.d == 64) return launch_d<64, WALK_STRIPED>(ap, m, num_sms, s);
+        return BA_ERR_SHAPE;
+    }
+    if (a.g.d == 128) return launch_d<128, WALK_PLAIN>(ap, m, num_sms, s);
+    if (a.g.d == 64) return launch_d<64, WALK_PLAIN>(ap, m, num_sms, s);
     return BA_ERR_SHAPE;
 }
 

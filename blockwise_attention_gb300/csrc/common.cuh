@@ -15,6 +15,11 @@ constexpr unsigned ERR_TIMEOUT_BIT = 1u;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
+// How a query tile walks the keys (template parameter S of the geometry
+// functions): every position of the ranks or of the block; the striped ring; a
+// sliding window behind the first keys (sinks).
+constexpr int WALK_PLAIN = 0, WALK_STRIPED = 1, WALK_WINDOW = 2;
+
 // ---------------------------------------------------------------------------
 // Geometry
 // ---------------------------------------------------------------------------
@@ -44,9 +49,19 @@ constexpr float LN2 = 0.6931471805599453f;
 // without it (c > r), and "key position <= query position" holds as in the
 // other partitions.  Masks are indexed by token and are not taken here.
 //
-// The geometry functions below take the striped choice as a template
-// parameter S (instantiated from g.striped by the launching code), so that the
-// kernels of the other partitions compile without it.
+// Window (g.window > 0; block mode with k_off = 0, causal): query p sees the
+// keys j <= p with j > p - window or j < sinks.  A query tile's walk is then one
+// chunk, or two when the window starts behind the sinks: the sink keys [0, sinks),
+// then the keys from `lo` to the last row's position, with lo a multiple of 128
+// before the first row (the number of tiles is that of the tightest start, and the
+// tiles' edges keep the alignment of the causal diagonal).  Every tile of the walk
+// is taken, also one that the mask empties (a cache shorter than the queries'
+// positions), so that its length is a formula.  Query heads h share the keys of
+// head h / kv_group.
+//
+// The geometry functions below take the choice as a template parameter S
+// (WALK_*, instantiated by the launching code), so that the kernels of the other
+// walks compile without it.
 struct Geom {
     int B, H, d;
     int ring;
@@ -68,6 +83,8 @@ struct Geom {
     const uint8_t *am;
     long long am_ld;
     const int8_t *cls;       // (B, n_qtiles, n_ktiles) classes, or nullptr (causal only)
+    int window, sinks;       // WALK_WINDOW: visible keys (p - window, p] and [0, sinks)
+    int kv_group;            // query heads per key head (WALK_WINDOW)
 };
 
 struct QTile {
@@ -94,7 +111,7 @@ __host__ __device__ inline int chunk_owner(const Geom &g, int c) {
 }
 
 // Query tile with id qg (0 .. n_qtiles-1) of head (b, h).
-template <bool S>
+template <int S>
 __host__ __device__ inline QTile q_tile(const Geom &g, int qg, int b, int h) {
     QTile t;
     t.g = qg;
@@ -105,7 +122,7 @@ __host__ __device__ inline QTile q_tile(const Geom &g, int qg, int b, int h) {
         t.row0 = c * g.CL + i * TILE;
         int end = (c + 1) * g.CL;
         t.len = (t.row0 + TILE < end ? t.row0 + TILE : end) - t.row0;
-        t.pos0 = S ? i * TILE : t.row0;   // striped: local index within the rank
+        t.pos0 = S == WALK_STRIPED ? i * TILE : t.row0;   // striped: local index within the rank
         t.rank = chunk_owner(g, c);
     } else {
         t.row0 = qg * TILE;
@@ -157,12 +174,12 @@ struct KWalk {
 // Position of the first key of chunk c for a query tile of rank qrank: its
 // global position, or in the striped ring its local index 0 shifted by one
 // when the key's rank follows the query's (see Geom).
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ int chunk_pos0(const Geom &g, int c, int qrank) {
-    return S ? (c > qrank ? 1 : 0) : c * g.CL;
+    return S == WALK_STRIPED ? (c > qrank ? 1 : 0) : c * g.CL;
 }
 
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ void kwalk_set_chunk(const Geom &g, KWalk &w, int c) {
     w.row = c * g.CL;
     w.chunk_end = w.row + g.CL;
@@ -170,12 +187,36 @@ __host__ __device__ __forceinline__ void kwalk_set_chunk(const Geom &g, KWalk &w
     w.pos_off = chunk_pos0<S>(g, c, w.qrank) - w.row;
 }
 
-template <bool S>
+// First key of the window walk of a tile whose first row is at position q_first.
+__host__ __device__ __forceinline__ int window_lo(const Geom &g, int q_first) {
+    const long long lo = (long long)q_first - (long long)TILE * (((long long)g.window - 1 + TILE - 1) / TILE);
+    return lo > g.sinks ? (int)lo : 0;   // inside or next to the sinks: one chunk from key 0
+}
+
+// Class of keys [k_first, k_last] for the rows q_first .. q_last under the window.
+__host__ __device__ __forceinline__ int window_class(const Geom &g, int q_first, int q_last, int k_first, int k_last) {
+    if (k_first > q_last || ((long long)k_last + g.window <= q_first && k_first >= g.sinks)) return BA_TILE_EMPTY;
+    if (k_last <= q_first && ((long long)k_first + g.window > q_last || k_last < g.sinks)) return BA_TILE_FULL;
+    return BA_TILE_PARTIAL;
+}
+
+template <int S>
 __host__ __device__ __forceinline__ void kwalk_begin(const Geom &g, const QTile &q, KWalk &w) {
     w.q_first = (int)q.pos0;
     w.q_last = (int)q.pos0 + q.len - 1;
     w.ci = 0;
     w.qrank = q.rank;
+    if constexpr (S == WALK_WINDOW) {
+        const int lo = window_lo(g, w.q_first), end = w.q_last + 1 < g.Lk ? w.q_last + 1 : g.Lk;
+        w.pos_off = 0;
+        w.idx = 0;
+        w.src = lo;          // the second chunk is [src, s)
+        w.s = end;
+        w.ci = lo > 0 ? 0 : 1;   // 1: the walk's last chunk
+        w.row = 0;
+        w.chunk_end = lo > 0 ? (g.sinks < end ? g.sinks : end) : end;
+        return;
+    }
     if (g.ring) {
         w.pos_off = 0;
         w.s = g.s_begin;
@@ -198,8 +239,15 @@ __host__ __device__ __forceinline__ void kwalk_begin(const Geom &g, const QTile 
 }
 
 // Moves to the next chunk of the walk; false when the walk is over.
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ bool kwalk_next_chunk(const Geom &g, KWalk &w) {
+    if constexpr (S == WALK_WINDOW) {
+        if (w.ci) return false;
+        w.ci = 1;
+        w.row = w.src;
+        w.chunk_end = w.s;
+        return true;
+    }
     if (!g.ring) return false;
     if (g.zigzag && w.ci == 0) {
         w.ci = 1;
@@ -214,7 +262,7 @@ __host__ __device__ __forceinline__ bool kwalk_next_chunk(const Geom &g, KWalk &
 }
 
 // Next non-EMPTY key tile of the walk into k; false at the end.
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ bool kwalk_next(const Geom &g, const QTile &q, KWalk &w, KTile &k) {
     for (;;) {
         if (w.row >= w.chunk_end) {
@@ -230,6 +278,11 @@ __host__ __device__ __forceinline__ bool kwalk_next(const Geom &g, const QTile &
         k.idx = w.idx;
         w.row = row + TILE;
         ++w.idx;
+        if constexpr (S == WALK_WINDOW) {
+            k.cls = window_class(g, w.q_first, w.q_last, pos, pos + k.len - 1);
+            if (k.cls == BA_TILE_FULL && g.kpm) k.cls = BA_TILE_PARTIAL;
+            return true;
+        }
         if (g.cls) {
             k.cls = g.cls[((long long)q.b * g.n_qtiles + q.g) * g.n_ktiles + k.idx];
             if (k.cls == BA_TILE_EMPTY) continue;
@@ -253,8 +306,14 @@ __host__ __device__ __forceinline__ bool kwalk_next(const Geom &g, const QTile &
 // this is a sum over the walk's chunks (a chunk contributes its tiles that start
 // at or before q's last row under causal masking, all of them otherwise), so it
 // costs a few operations per chunk instead of a walk over every tile.
-template <bool S>
+template <int S>
 __host__ __device__ inline int kwalk_count(const Geom &g, const QTile &q) {
+    if constexpr (S == WALK_WINDOW) {
+        const int lo = window_lo(g, (int)q.pos0);
+        const int last = (int)q.pos0 + q.len, end = last < g.Lk ? last : g.Lk;
+        const int first = lo > 0 ? (g.sinks < end ? g.sinks : end) : 0;
+        return (first + TILE - 1) / TILE + (end > lo ? (end - lo + TILE - 1) / TILE : 0);
+    }
     if (g.cls) {
         KWalk w;
         kwalk_begin<S>(g, q, w);
@@ -284,23 +343,23 @@ __host__ __device__ inline int kwalk_count(const Geom &g, const QTile &q) {
 
 // Token of row R of a ring tensor: R itself, or r + P u for row R = r CL + u
 // of the striped ring.
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ long long row_token(const Geom &g, long long R) {
-    if (!S) return R;
+    if (S != WALK_STRIPED) return R;
     const long long r = R / g.CL;
     return r + (long long)g.P * (R - r * g.CL);
 }
 
 // Row of out / lse (token order) for row `row` of query tile q.
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ long long out_row(const Geom &g, const QTile &q, int row) {
-    return S ? q.rank + (long long)g.P * (q.pos0 + row) : (long long)q.row0 + row;
+    return S == WALK_STRIPED ? q.rank + (long long)g.P * (q.pos0 + row) : (long long)q.row0 + row;
 }
 
 // Work item w -> (q tile, b, h).  Items are grouped by heads_per_group (b, h)
 // pairs so that concurrently running CTAs share K/V in L2; within a group the
 // query tiles come heaviest first under causal masking (latest positions).
-template <bool S>
+template <int S>
 __host__ __device__ inline QTile work_item(const Geom &g, int w) {
     int BH = g.B * g.H;
     int G = g.heads_per_group;
@@ -315,8 +374,10 @@ __host__ __device__ inline QTile work_item(const Geom &g, int w) {
 }
 
 // Is key position kp excluded for query position qp of batch item b?
+template <int S = WALK_PLAIN>
 __device__ inline bool excluded(const Geom &g, int b, long long qp, long long kp) {
     if (g.causal && kp > qp) return true;
+    if (S == WALK_WINDOW && kp <= qp - g.window && kp >= g.sinks) return true;
     if (g.kpm && g.kpm[b * g.kpm_ld + kp]) return true;
     if (g.am && g.am[qp * g.am_ld + kp]) return true;
     return false;
@@ -355,7 +416,7 @@ __host__ __device__ inline int n_pairs(const Geom &g) {
 // that concurrently running CTAs share K/V in L2.  Phase 2 deals the lightest
 // levels of all heads, heaviest first: the items claimed last are the smallest
 // of the launch, so the CTAs finish within about one small item of each other.
-template <bool S>
+template <int S>
 __host__ __device__ inline QPair work_pair(const Geom &g, int w) {
     const int BH = g.B * g.H, G = g.heads_per_group, np = n_pairs(g);
     const int tail = g.tail_levels < np ? g.tail_levels : np;
@@ -374,7 +435,7 @@ __host__ __device__ inline QPair work_pair(const Geom &g, int w) {
     }
     const int ppc = pairs_per_chunk(g), per = g.ring ? g.nqt_pc : g.n_qtiles;
     int c, i;
-    if (S && g.causal) {
+    if (S == WALK_STRIPED && g.causal) {
         // a query at local index u of rank r sees P u + r + 1 keys: deal the
         // levels of all ranks together, last level and last rank first
         c = g.NC - 1 - pi % g.NC;
@@ -400,7 +461,7 @@ __host__ __device__ inline QPair work_pair(const Geom &g, int w) {
 
 // Next key tile of the pair's walk that one of its query tiles sees, with the
 // class for each (c1 = EMPTY when the pair holds one tile); false at the end.
-template <bool S>
+template <int S>
 __host__ __device__ __forceinline__ bool pair_next(const Geom &g, const QPair &p, KWalk &w, KTile &k, int &c0,
                                               int &c1) {
     const int q0_last = (int)p.q0.pos0 + p.q0.len - 1;
@@ -419,6 +480,16 @@ __host__ __device__ __forceinline__ bool pair_next(const Geom &g, const QPair &p
         k.idx = w.idx;
         w.row = row + TILE;
         ++w.idx;
+        if constexpr (S == WALK_WINDOW) {
+            const int k_last = pos + k.len - 1;
+            c0 = window_class(g, (int)p.q0.pos0, q0_last, pos, k_last);
+            c1 = has1 ? window_class(g, (int)p.q1.pos0, (int)p.q1.pos0 + p.q1.len - 1, pos, k_last) : BA_TILE_EMPTY;
+            if (g.kpm) {
+                if (c0 == BA_TILE_FULL) c0 = BA_TILE_PARTIAL;
+                if (c1 == BA_TILE_FULL) c1 = BA_TILE_PARTIAL;
+            }
+            return true;
+        }
         if (g.cls) {
             const int8_t *m = g.cls + ((long long)p.q0.b * g.n_qtiles + p.q0.g) * g.n_ktiles + k.idx;
             c0 = m[0];
@@ -447,7 +518,7 @@ __host__ __device__ __forceinline__ bool pair_next(const Geom &g, const QPair &p
 }
 
 // Number of key tiles pair_next yields for pair p.
-template <bool S>
+template <int S>
 __host__ __device__ inline int pair_count(const Geom &g, const QPair &p) {
     if (!g.cls) return kwalk_count<S>(g, p.span);   // the span's walk: both tiles see a tile the span sees
     KWalk w;

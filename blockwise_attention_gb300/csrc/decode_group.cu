@@ -1,0 +1,770 @@
+// Single-token attention with grouped heads: a window with sinks over a bf16 or fp32
+// cache (attn_window_decode_fwd), and the whole cache or a window over a cache held in
+// 4 bits (attn_decode_kv4_fwd).
+//
+// Sequence b holds len = lengths[b] keys and its query is at position len - 1.  The
+// keys it sees, [0, s) and [lo, len) with lo = len - window behind the s = sinks first
+// ones (all of [0, len) when lo <= sinks), are numbered 0 .. n - 1 without a gap; the
+// softmax does not mind the order.  That range is cut into splits; a CTA takes one
+// split of one key head for all (up to 16) query heads that share it, so that every
+// key is read once, and each split's (O, m, l) is joined with the others' by the rule
+// of attn_merge in a second, small launch (none when there is one split).
+//
+// decode_mma_kernel (bf16 cache with d = 64, 128; 4-bit cache).  What bounds it is HBM:
+//   a key costs 4 G d flop for 4 d bytes (bf16) or 1.125 d bytes (4 bits), G <= 16.  On
+//   the CUDA cores that would be 2 G d FMAs a key, beyond the fp32 rate from about G = 4
+//   at 6.8 TB/s; the products therefore run as mma.sync m16n8k16 with the query heads as
+//   M.  (tcgen05.mma needs 128 rows of M or N and its operands in shared memory in its
+//   own layout, which for the 4-bit cache would mean writing every unpacked value back
+//   to shared memory; here the fragments are unpacked in the registers that loaded
+//   them.)  A warp works alone on tiles of 16 keys, which it brings in with cp.async
+//   through a ring of its own in shared memory: every lane copies exactly the bytes that
+//   it will use and reads them back itself, so the loop has no block barrier.
+//   Fragments: the order of d inside the contraction q . k and that of the columns of O
+//   are free, so a lane (g = lane / 4, t = lane % 4) takes contiguous runs: of key g the
+//   d's of t for K, and of the keys 2t, 2t+1, 2t+8, 2t+9 the d's of g for V; the pairs of
+//   keys that the P V fragment wants side by side are put together with byte permutes.
+//   4 bits: a code times its e4m3 scale has 6 significant bits, so the unpacked values are
+//   exact in fp16; q is scaled by a power of two to at most 2 in magnitude before its
+//   conversion (bf16 values keep their 8 bits down to 2^-14 of the largest), and p is
+//   kept times 2^11 in fp16 (relative 2^-11, absolute 2^-36 of the row's largest).
+//   bf16: p is rounded to bf16 for P V, as in the prompt kernels.  l sums unrounded p.
+//
+// decode_simt_kernel (fp32, and bf16 with d = 16, 32): lanes own 16 bytes of a key row,
+//   fp32 arithmetic, up to four query heads at a time.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace ba {
+namespace {
+
+constexpr int DG_WARPS = 4;
+constexpr float P_BIAS = 11.f;      // 4-bit cache: p is kept times 2^P_BIAS
+constexpr float LAZY = 4.f;         // the reference maximum moves when exceeded by 2^LAZY
+
+// The visible keys of one sequence as a gapless range of n indices.
+struct KeyRange {
+    int n, s;          // indices; the first s are the slots 0 .. s - 1
+    long long shift;   // slot of index i >= s: i + shift
+    __device__ __forceinline__ long long slot(int i) const { return i < s ? i : i + shift; }
+};
+
+__device__ __forceinline__ KeyRange key_range(const DecodeGroupArgs &a, int b) {
+    const int len = a.lengths ? min(max(a.lengths[b], 0), a.S) : a.S;
+    KeyRange r;
+    const int lo = a.window > 0 ? len - a.window : 0;
+    if (lo <= a.sinks) {
+        r.n = len;
+        r.s = 0;
+        r.shift = 0;
+    } else {
+        r.s = a.sinks;
+        r.n = a.sinks + len - lo;
+        r.shift = lo - a.sinks;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void *src, bool in) {   // 4 or 8 bytes
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? N : 0), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4b(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds2b(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1b(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), 16-bit operands of one type.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (F16)
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The eight e2m1 codes of a word as four fp16 pairs (the low nibble of a byte in the low half).
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&o)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+// Two e4m3 scales (low byte first) as an fp16 pair.
+__device__ __forceinline__ uint32_t scales2(uint32_t two) {
+    uint32_t o;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o) : "h"((uint16_t)two));
+    return o;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t o;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    return o;
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
+    uint32_t o;
+    if (f16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+    return o;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a split found for element d of query head h: the reference maximum ref (log2
+// units), the sum L and the weighted sum acc relative to it.  One split: the result.
+__device__ __forceinline__ void store_split(const DecodeGroupArgs &a, int b, int h, int split, int d, float ref, float L,
+                                            float acc) {
+    const long long row = (long long)b * a.Hkv * a.G + h;
+    if (a.n_splits > 1) {
+        a.part_o[(row * a.n_splits + split) * a.d + d] = acc;
+        if (d == 0) a.part_ml[row * a.n_splits + split] = make_float2(ref, L);
+        return;
+    }
+    const float y = L > 0.f ? acc / L * a.out_mul : 0.f;
+    if (a.out_dtype == BA_BF16)
+        static_cast<__nv_bfloat16 *>(a.out)[row * a.d + d] = __float2bfloat16_rn(L != L ? L : y);
+    else
+        static_cast<float *>(a.out)[row * a.d + d] = L != L ? L : y;
+    if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (ref + log2f(L)) * LN2;
+}
+
+// One stage of a warp's ring: a tile of 16 keys, in the order in which the lanes read it.
+template <int D, bool KV4>
+struct Ring {
+    // bf16: K as [key half][chunk of 32 d's][lane] and V as [key 0..3 of the lane][chunk of 64 d's][lane], 16 bytes each.
+    // 4 bits: K as [key half][lane] (D / 8 bytes), V as [key 0..3][lane] (D / 16 bytes), then the 16 keys' scales of K and V.
+    static constexpr int K_BYTES = KV4 ? 2 * 32 * (D / 8) : 2 * (D / 32) * 512;
+    static constexpr int V_BYTES = KV4 ? 4 * 32 * (D / 16) : 4 * (D / 64) * 512;
+    static constexpr int SC_ROW = D / 16;
+    static constexpr int SC_BYTES = KV4 ? 2 * 16 * SC_ROW : 0;
+    static constexpr int STAGE = K_BYTES + V_BYTES + SC_BYTES;
+    static constexpr int NS = KV4 ? 6 : 3;
+    static constexpr int BYTES = DG_WARPS * NS * STAGE;
+};
+
+template <int D, bool KV4, int HALVES>
+__global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeGroupArgs a) {
+    using R = Ring<D, KV4>;
+    constexpr int NT = D / 8;    // column tiles of O
+    constexpr int KS = D / 16;   // steps of the contraction over d
+    extern __shared__ __align__(128) uint8_t dg_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x, bh = blockIdx.y, b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int h0 = blockIdx.z * 16, nh = min(16, a.G - h0);   // query heads hk G + h0 .. of this CTA
+    const KeyRange kr = key_range(a, b);
+    const int v0 = split * a.split_len, v1 = min(kr.n, v0 + a.split_len);
+    if (v0 >= v1 && a.n_splits > 1) return;   // the join reads the splits that hold keys
+
+    // q fragments: the d's that lane t contracts, in the order of its K words.  4 bits:
+    // times a power of two that brings the row's largest magnitude into [1, 2).
+    uint32_t qa[KS][2 * HALVES];   // [step][2 half + k half]
+    float sl2[2] = {a.scale_log2, a.scale_log2};
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) {
+        const int row = g + 8 * hf;
+        uint32_t w[2 * KS];
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (long long)b * a.qsB +
+                                  (long long)(hk * a.G + h0 + min(row, nh - 1)) * a.qsH;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const int d0 = KV4 ? t * (D / 4) + c * 8 : c * 32 + t * 8;
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(qp + d0));
+            w[4 * c] = u.x;
+            w[4 * c + 1] = u.y;
+            w[4 * c + 2] = u.z;
+            w[4 * c + 3] = u.w;
+        }
+        if constexpr (KV4) {
+            uint32_t big = 0;   // largest magnitude, as bits
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int e = min(max((int)(big >> 7), 1), 253);   // biased exponent
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+            sl2[hf] *= up;
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i)
+                w[i] = pack16(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down, true);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qa[s][2 * hf] = row < nh ? w[2 * s] : 0u;
+            qa[s][2 * hf + 1] = row < nh ? w[2 * s + 1] : 0u;
+        }
+    }
+
+    const uint32_t ring = smem_u32(dg_smem) + (uint32_t)warp * R::NS * R::STAGE;
+    const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH;
+    const uint8_t *vb = static_cast<const uint8_t *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH;
+    const uint8_t *ksb = KV4 ? static_cast<const uint8_t *>(a.k_scales) + (long long)b * a.kcB + (long long)hk * a.kcH : nullptr;
+    const uint8_t *vsb = KV4 ? static_cast<const uint8_t *>(a.v_scales) + (long long)b * a.vcB + (long long)hk * a.vcH : nullptr;
+
+    // Tile i of this warp: indices v0 + 16 (warp + DG_WARPS i) ..; keys behind v1 are
+    // not read (their bytes arrive as zeros).
+    const int tiles = v1 > v0 ? (v1 - v0 + 15) / 16 : 0;
+    const int mine = tiles > warp ? (tiles - warp + DG_WARPS - 1) / DG_WARPS : 0;
+    auto issue = [&](int i) {
+        if (i < mine) {
+            const uint32_t st = ring + (uint32_t)(i % R::NS) * R::STAGE;
+            const int i0 = v0 + 16 * (warp + DG_WARPS * i);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int idx = i0 + 8 * n + g;
+                const uint8_t *row = kb + kr.slot(min(idx, v1 - 1)) * a.ksT;
+                if constexpr (KV4) {
+                    if constexpr (D == 128)
+                        cp16(st + (n * 32 + lane) * 16, row + t * 16, idx < v1);
+                    else
+                        cp_small<8>(st + (n * 32 + lane) * 8, row + t * 8, idx < v1);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        cp16(st + ((n * (D / 32) + c) * 32 + lane) * 16, row + c * 64 + t * 16, idx < v1);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int idx = i0 + 2 * t + (u & 1) + 8 * (u >> 1);
+                const uint8_t *row = vb + kr.slot(min(idx, v1 - 1)) * a.vsT;
+                if constexpr (KV4) {
+                    cp_small<D / 16>(st + R::K_BYTES + (u * 32 + lane) * (D / 16), row + g * (D / 16), idx < v1);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        cp16(st + R::K_BYTES + ((u * (D / 64) + c) * 32 + lane) * 16, row + c * 128 + g * 16, idx < v1);
+                }
+            }
+            if constexpr (KV4) {   // lanes 0 .. 15 the keys' scales of K, 16 .. 31 of V
+                const int idx = i0 + (lane & 15);
+                const long long slot = kr.slot(min(idx, v1 - 1));
+                const uint8_t *row = lane < 16 ? ksb + slot * a.kcT : vsb + slot * a.vcT;
+                cp_small<R::SC_ROW>(st + R::K_BYTES + R::V_BYTES + lane * R::SC_ROW, row, idx < v1);
+            }
+        }
+        cp_commit();   // a group each time, so that the counts below hold
+    };
+#pragma unroll
+    for (int i = 0; i < R::NS - 1; ++i) issue(i);
+
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+
+    for (int i = 0; i < mine; ++i) {
+        issue(i + R::NS - 1);     // into the stage of tile i - 1, which every lane has read (__syncwarp below)
+        cp_wait<R::NS - 1>();     // tile i has arrived
+        __syncwarp();             // for every lane: the scales are shared
+        const uint32_t st = ring + (uint32_t)(i % R::NS) * R::STAGE;
+        const int i0 = v0 + 16 * (warp + DG_WARPS * i);
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            uint32_t kw[2 * KS];
+            if constexpr (KV4) {
+                uint32_t code[D / 32];
+                const uint32_t sc_at = st + R::K_BYTES + R::V_BYTES + (8 * n + g) * R::SC_ROW;
+                uint32_t sc[2];   // the scale of each 16 codes of the lane, twice in a word
+                if constexpr (D == 128) {
+                    const uint4 u = lds16(st + (n * 32 + lane) * 16);
+                    code[0] = u.x;
+                    code[1] = u.y;
+                    code[2] = u.z;
+                    code[3] = u.w;
+                    const uint32_t p = scales2(lds2b(sc_at + 2 * t));
+                    sc[0] = __byte_perm(p, p, 0x1010);
+                    sc[1] = __byte_perm(p, p, 0x3232);
+                } else {
+                    const uint2 u = lds8(st + (n * 32 + lane) * 8);
+                    code[0] = u.x;
+                    code[1] = u.y;
+                    const uint32_t p = scales2(lds1b(sc_at + t));
+                    sc[0] = sc[1] = __byte_perm(p, p, 0x1010);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t f[4];
+                    unpack8(code[c], f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kw[4 * c + e] = hmul2(f[e], sc[c >> 1]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const uint4 u = lds16(st + ((n * (D / 32) + c) * 32 + lane) * 16);
+                    kw[4 * c] = u.x;
+                    kw[4 * c + 1] = u.y;
+                    kw[4 * c + 2] = u.z;
+                    kw[4 * c + 3] = u.w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                mma16816<KV4>(s[n], qa[k][0], HALVES == 2 ? qa[k][2 * HALVES - 2] : 0u, qa[k][1],
+                              HALVES == 2 ? qa[k][2 * HALVES - 1] : 0u, kw[2 * k], kw[2 * k + 1]);
+        }
+        // scores in log2 units; indices behind the range take no part
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool in = i0 + 8 * n + 2 * t + e < v1;
+#pragma unroll
+                for (int hf = 0; hf < HALVES; ++hf) {
+                    float &x = s[n][2 * hf + e];
+                    x = in ? x * sl2[hf] : -INFINITY;
+                    mx[hf] = fmaxf(mx[hf], x);
+                }
+            }
+        bool move = false;
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
+            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
+            move = move || mx[hf] > m[hf] + LAZY;
+        }
+        // The reference maximum moves, and O and l with it, only when a row's maximum
+        // passes it by more than 2^LAZY; p stays below 2^LAZY until then.
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf) {
+                const float m_new = fmaxf(m[hf], mx[hf]);
+                const float alpha = m_new == -INFINITY ? 1.f : ex2(m[hf] - m_new);
+                m[hf] = m_new;
+                l[hf] *= alpha;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[n][2 * hf] *= alpha;
+                    o[n][2 * hf + 1] *= alpha;
+                }
+            }
+        }
+        uint32_t pa[2][2];   // [key half][row half]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            if (hf >= HALVES) {
+                pa[0][hf] = pa[1][hf] = 0u;
+                continue;
+            }
+            const float base = (m[hf] == -INFINITY ? 0.f : m[hf]) - (KV4 ? P_BIAS : 0.f);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float p0 = ex2(s[n][2 * hf] - base), p1 = ex2(s[n][2 * hf + 1] - base);
+                l[hf] += p0 + p1;
+                pa[n][hf] = pack16(p0, p1, KV4);
+            }
+        }
+        if constexpr (KV4) {
+            constexpr int VW = D / 64;   // words of codes per key and lane
+            uint32_t vw[4][VW], vs[2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t at = st + R::K_BYTES + (u * 32 + lane) * (D / 16);
+                if constexpr (VW == 2) {
+                    const uint2 x = lds8(at);
+                    vw[u][0] = x.x;
+                    vw[u][1] = x.y;
+                } else {
+                    vw[u][0] = lds4b(at);
+                }
+            }
+            const uint32_t sc_at = st + R::K_BYTES + R::V_BYTES + 16 * R::SC_ROW + (D == 128 ? g : g >> 1);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)   // scales of the keys 2t + 8u, 2t + 1 + 8u
+                vs[u] = scales2(lds1b(sc_at + (2 * t + 8 * u) * R::SC_ROW) | lds1b(sc_at + (2 * t + 1 + 8 * u) * R::SC_ROW) << 8);
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                uint32_t even[2][4], odd[2][4];   // [key half]: (key 2t, key 2t + 1) of the word's even and odd d's
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t x = vw[2 * u][w], y = vw[2 * u + 1][w];
+                    unpack8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), even[u]);
+                    unpack8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd[u]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mma16816<true>(o[8 * w + 2 * e], pa[0][0], pa[0][1], pa[1][0], pa[1][1], hmul2(even[0][e], vs[0]),
+                                   hmul2(even[1][e], vs[1]));
+                    mma16816<true>(o[8 * w + 2 * e + 1], pa[0][0], pa[0][1], pa[1][0], pa[1][1], hmul2(odd[0][e], vs[0]),
+                                   hmul2(odd[1][e], vs[1]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t vw[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 x = lds16(st + R::K_BYTES + ((u * (D / 64) + c) * 32 + lane) * 16);
+                    vw[u][0] = x.x;
+                    vw[u][1] = x.y;
+                    vw[u][2] = x.z;
+                    vw[u][3] = x.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+                    mma16816<false>(o[8 * c + e], pa[0][0], pa[0][1], pa[1][0], pa[1][1],
+                                    __byte_perm(vw[0][e >> 1], vw[1][e >> 1], sel),
+                                    __byte_perm(vw[2][e >> 1], vw[3][e >> 1], sel));
+                }
+            }
+        }
+        __syncwarp();   // the stage may be refilled
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be placed now
+    cp_wait<0>();
+    __syncthreads();   // every warp is done with its ring: the merge area overlays it
+
+    // Join the warps: row r's (m, l) and O of each warp, then one weighted sum.
+    float *mo = reinterpret_cast<float *>(dg_smem);                    // [warp][16][D]
+    float *mm = mo + DG_WARPS * 8 * HALVES * D, *ml = mm + DG_WARPS * 16;   // [warp][16]
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) {
+        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
+        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
+        const int row = g + 8 * hf;
+        if (t == 0) {
+            mm[warp * 16 + row] = m[hf];
+            ml[warp * 16 + row] = l[hf];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // column 2t + e of tile n belongs to the d's of lane group 2t + e
+                const int gg = 2 * t + e;
+                const int d = KV4 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
+                mo[(warp * 8 * HALVES + row) * D + d] = o[n][2 * hf + e];
+            }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < nh * D; x += DG_WARPS * 32) {
+        const int row = x / D, d = x % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < DG_WARPS; ++w) M = fmaxf(M, mm[w * 16 + row]);
+        float L = 0.f, acc = 0.f;
+        if (M != -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < DG_WARPS; ++w) {
+                const float wt = ex2(mm[w * 16 + row] - M);
+                L += wt * ml[w * 16 + row];
+                acc += wt * mo[(w * 8 * HALVES + row) * D + d];
+            }
+        }
+        store_split(a, b, hk * a.G + h0 + row, split, d, M - (KV4 ? P_BIAS : 0.f), L, acc);
+    }
+}
+
+// fp32 arithmetic: a group of LPK lanes owns a key, each lane 16 bytes of its row; the
+// query heads h0 .. h0 + HC - 1 share the loads.  The groups of the CTA are joined in
+// shared memory.
+template <typename T>
+struct Row16;   // 16 bytes of T, unpacked to fp32
+template <>
+struct Row16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ __forceinline__ static void load(const void *p, float (&x)[8]) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Row16<float> {
+    static constexpr int N = 4;
+    __device__ __forceinline__ static void load(const void *p, float (&x)[4]) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(p));
+        x[0] = u.x;
+        x[1] = u.y;
+        x[2] = u.z;
+        x[3] = u.w;
+    }
+};
+
+template <typename T, int D, int HC>
+__global__ void __launch_bounds__(128) decode_simt_kernel(const DecodeGroupArgs a) {
+    constexpr int EPL = Row16<T>::N, LPK = D / EPL, GROUPS = 128 / LPK, GPW = 32 / LPK, UN = 4;
+    __shared__ float sm_o[GROUPS][HC][D];
+    __shared__ float sm_m[GROUPS][HC], sm_l[GROUPS][HC];
+    const int split = blockIdx.x, bh = blockIdx.y, b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int h0 = blockIdx.z * HC, nh = min(HC, a.G - h0);
+    const KeyRange kr = key_range(a, b);
+    const int v0 = split * a.split_len, v1 = min(kr.n, v0 + a.split_len);
+    if (v0 >= v1 && a.n_splits > 1) return;
+    const int grp = threadIdx.x / LPK, gl = threadIdx.x % LPK;
+    const int warp = threadIdx.x / 32, gw = (threadIdx.x % 32) / LPK;
+
+    float q[HC][EPL], o[HC][EPL], m[HC], l[HC];
+#pragma unroll
+    for (int h = 0; h < HC; ++h) {
+        const T *qp = static_cast<const T *>(a.q) + (long long)b * a.qsB +
+                      (long long)(hk * a.G + h0 + min(h, nh - 1)) * a.qsH;
+        Row16<T>::load(qp + gl * EPL, q[h]);
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) o[h][e] = 0.f;
+    }
+    const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH + gl * 16;
+    const uint8_t *vb = static_cast<const uint8_t *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH + gl * 16;
+
+    // The loop runs on a warp-uniform base (the shuffles span the warp); keys behind the
+    // range are masked and their loads clamped into it.
+    for (int jb = v0 + warp * GPW * UN; jb < v1; jb += 4 * GPW * UN) {
+        const int j0 = jb + gw * UN;
+        float kx[UN][EPL], vx[UN][EPL];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const long long slot = kr.slot(min(j0 + u, v1 - 1));
+            Row16<T>::load(kb + slot * a.ksT, kx[u]);
+            Row16<T>::load(vb + slot * a.vsT, vx[u]);
+            if (j0 + u >= v1) {   // a repeated key: no part of it may enter the sums
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) vx[u][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < HC; ++h) {
+            float s[UN], mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                float acc = 0.f;
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) acc = fmaf(q[h][e], kx[u][e], acc);
+#pragma unroll
+                for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off, LPK);
+                s[u] = j0 + u < v1 ? acc * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[u]);
+            }
+            const float m_new = fmaxf(m[h], mx);
+            const float alpha = m[h] == -INFINITY ? 0.f : exp2f(m[h] - m_new);
+            l[h] *= alpha;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) o[h][e] *= alpha;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const float p = s[u] == -INFINITY ? 0.f : exp2f(s[u] - m_new);
+                l[h] += p;
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) o[h][e] = fmaf(p, vx[u][e], o[h][e]);
+            }
+            m[h] = m_new;
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < HC; ++h) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) sm_o[grp][h][gl * EPL + e] = o[h][e];
+        if (gl == 0) {
+            sm_m[grp][h] = m[h];
+            sm_l[grp][h] = l[h];
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < nh * D; x += 128) {
+        const int h = x / D, d = x % D;
+        float M = -INFINITY, L = 0.f, acc = 0.f;
+        for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, sm_m[g][h]);
+        if (M != -INFINITY) {
+            for (int g = 0; g < GROUPS; ++g) {
+                const float w = exp2f(sm_m[g][h] - M);
+                L += w * sm_l[g][h];
+                acc += w * sm_o[g][h][d];
+            }
+        }
+        store_split(a, b, hk * a.G + h0 + h, split, d, M, L, acc);
+    }
+}
+
+// The join of a row's splits: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  One block
+// per (b, query head); it is launched while the splits still run (programmatic launch)
+// and waits for them, so that its start is hidden.
+__global__ void __launch_bounds__(128) decode_join_kernel(const DecodeGroupArgs a) {
+    __shared__ float wt[128], red[4];
+    const int b = blockIdx.x / (a.Hkv * a.G), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = blockIdx.x;
+    const int n = key_range(a, b).n;
+    const int used = (n + a.split_len - 1) / a.split_len;   // the splits that hold keys
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float M = -INFINITY, L = 0.f, acc = 0.f;
+    const float2 *ml = a.part_ml + row * a.n_splits;
+    const float *po = a.part_o + row * a.n_splits * a.d;
+    for (int s0 = 0; s0 < used; s0 += 128) {   // in rounds of 128 splits, carrying (M, L, acc)
+        const int here = min(128, used - s0);
+        const float2 x = threadIdx.x < here ? __ldcg(ml + s0 + threadIdx.x) : make_float2(-INFINITY, 0.f);
+        float v = x.x;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        __syncthreads();
+        if (lane == 0) red[warp] = v;
+        __syncthreads();
+        const float M_new = fmaxf(fmaxf(M, fmaxf(red[0], red[1])), fmaxf(red[2], red[3]));
+        const float carry = M == -INFINITY ? 0.f : exp2f(M - M_new);
+        const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - M_new);
+        float lw = w * x.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+        __syncthreads();
+        wt[threadIdx.x] = w;
+        if (lane == 0) red[warp] = lw;
+        __syncthreads();
+        L = L * carry + ((red[0] + red[1]) + (red[2] + red[3]));
+        if (threadIdx.x < a.d) {
+            acc *= carry;
+#pragma unroll 8
+            for (int s = 0; s < here; ++s) acc = fmaf(wt[s], __ldcg(po + (long long)(s0 + s) * a.d + threadIdx.x), acc);
+        }
+        M = M_new;
+    }
+    if (threadIdx.x < a.d) {
+        const float y = L > 0.f ? acc / L * a.out_mul : (L != L ? L : 0.f);
+        if (a.out_dtype == BA_BF16)
+            static_cast<__nv_bfloat16 *>(a.out)[row * a.d + threadIdx.x] = __float2bfloat16_rn(y);
+        else
+            static_cast<float *>(a.out)[row * a.d + threadIdx.x] = y;
+        if (threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+    }
+}
+
+template <int D, bool KV4, int HALVES>
+int launch_mma(const DecodeGroupArgs &a, cudaStream_t s) {
+    auto kern = decode_mma_kernel<D, KV4, HALVES>;
+    constexpr int merge = DG_WARPS * (8 * HALVES * D + 32) * 4;
+    constexpr int smem = Ring<D, KV4>::BYTES > merge ? Ring<D, KV4>::BYTES : merge;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BA_ERR_CUDA;
+    kern<<<dim3(a.n_splits, a.B * a.Hkv, (a.G + 15) / 16), DG_WARPS * 32, smem, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_simt(const DecodeGroupArgs &a, cudaStream_t s) {
+    const int hc = a.G >= 3 ? 4 : a.G;
+    const dim3 grid(a.n_splits, a.B * a.Hkv, (a.G + hc - 1) / hc);
+    if (hc == 4)
+        decode_simt_kernel<T, D, 4><<<grid, 128, 0, s>>>(a);
+    else if (hc == 2)
+        decode_simt_kernel<T, D, 2><<<grid, 128, 0, s>>>(a);
+    else
+        decode_simt_kernel<T, D, 1><<<grid, 128, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+}
+
+template <typename T>
+int launch_simt_t(const DecodeGroupArgs &a, cudaStream_t s) {
+    switch (a.d) {
+        case 16: return launch_simt<T, 16>(a, s);
+        case 32: return launch_simt<T, 32>(a, s);
+        case 64: return launch_simt<T, 64>(a, s);
+        case 128: return launch_simt<T, 128>(a, s);
+        default: return BA_ERR_SHAPE;
+    }
+}
+
+}  // namespace
+
+// The tensor-core kernel's case (else the CUDA-core one).
+static bool on_mma(int dtype, int d, bool kv4) { return kv4 || (dtype == BA_BF16 && (d == 64 || d == 128)); }
+
+// Key splits for B * Hkv ranges of up to n_max keys.  Long ranges are cut so that the
+// launch has about eight CTAs for each place on the GPU (the last, partly filled wave is
+// then a small part) but 512 keys at least, so that joining stays small beside reading;
+// when that leaves SMs idle, down to 64 keys (a tile for each warp).
+int decode_group_splits(int B, int Hkv, int G, long long n_max, bool kv4, int num_sms) {
+    const long long bh = (long long)B * Hkv * ((G + 15) / 16);
+    if (n_max <= 64 || bh == 0) return 1;
+    const long long places = (long long)num_sms * (kv4 ? 3 : 2);
+    long long n = (n_max + 511) / 512, want = (8 * places + bh - 1) / bh;
+    if (n > want) n = want;
+    if (n * bh < num_sms) {
+        n = (n_max + 63) / 64;
+        want = (num_sms + bh - 1) / bh;
+        if (n > want) n = want;
+    }
+    return (int)(n < 1 ? 1 : n);
+}
+
+int launch_decode_group(const DecodeGroupArgs &a, cudaStream_t s) {
+    const bool kv4 = a.k_scales != nullptr;
+    int rc;
+    if (on_mma(a.dtype, a.d, kv4)) {
+        const bool two = a.G > 8;
+        if (kv4)
+            rc = a.d == 128 ? (two ? launch_mma<128, true, 2>(a, s) : launch_mma<128, true, 1>(a, s))
+                            : (two ? launch_mma<64, true, 2>(a, s) : launch_mma<64, true, 1>(a, s));
+        else
+            rc = a.d == 128 ? (two ? launch_mma<128, false, 2>(a, s) : launch_mma<128, false, 1>(a, s))
+                            : (two ? launch_mma<64, false, 2>(a, s) : launch_mma<64, false, 1>(a, s));
+    } else {
+        rc = a.dtype == BA_BF16 ? launch_simt_t<__nv_bfloat16>(a, s) : launch_simt_t<float>(a, s);
+    }
+    if (rc || a.n_splits == 1) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.G));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel, a) == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+}
+
+}  // namespace ba

@@ -60,6 +60,13 @@ struct BwdArgs {
     unsigned long long wait_limit_ns;    // bounded-wait limit (tensor-core kernels)
     unsigned *sched;                     // 2 zeroed item counters (dK/dV kernel, dQ kernel), tensor-core kernels
     int heads_per_group;                 // (b, h) pairs whose items run side by side (L2 reuse)
+    // Sliding window with sinks (window > 0: block geometry with k_off = 0, causal).
+    int window, sinks;                   // visible keys (p - window, p] and [0, sinks)
+    int Hkv, kv_group;                   // key heads; query heads per key head
+    int grad_bf16;                       // gradients stored as bf16 (else fp32)
+    int n_sink_tiles;                    // key tiles that hold sinks: their queries are split into
+    int n_sink_parts, sink_rows;         //   n_sink_parts chunks of sink_rows query rows, one partial each
+    float *part;                         // (B, Hkv, n_sink_tiles, n_sink_parts, dV / dK, tile rows, d) partials
 };
 
 // TMA descriptors of q, k, v and dout for the tensor-core backward.
@@ -69,6 +76,9 @@ struct BwdMaps {
 
 int launch_attn_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_bwd_pre(const BwdArgs &a, int num_sms, cudaStream_t s);
+int launch_attn_window_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
+int launch_attn_window_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s);
+int launch_sink_sum(const BwdArgs &a, int tile_rows, int num_sms, cudaStream_t s);
 bool bwd_tc_supported(int dtype, int d);
 int launch_attn_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s);
 
@@ -102,6 +112,46 @@ struct DecodeArgs {
 };
 
 int launch_decode(const DecodeArgs &a, cudaStream_t s);
+
+// Decode attention of grouped heads over a window with sinks or a 4-bit cache, in key splits.
+struct DecodeGroupArgs {
+    int B, Hkv, G, S, d, dtype;          // Hkv G query heads; dtype of q (and of a cache that is not 4-bit)
+    const void *q, *k, *v;               // q: (B, Hkv G, 1, d), element strides; k, v: rows of the cache, BYTE strides
+    long long qsB, qsH;
+    long long ksB, ksH, ksT, vsB, vsH, vsT;
+    const void *k_scales, *v_scales;     // 4-bit cache: e4m3 scales, byte strides (null: k, v hold dtype)
+    long long kcB, kcH, kcT, vcB, vcH, vcT;
+    const int32_t *lengths;              // (B) valid cache lengths, or nullptr = S
+    int window, sinks;                   // window 0: every key
+    float scale_log2;                    // softmax scale * log2(e) (times the 4-bit keys' power of two)
+    float out_mul;                       // factor of the outputs (the 4-bit values' power of two)
+    int split_len, n_splits;
+    float *part_o;                       // (B Hq, n_splits, d) weighted sums
+    float2 *part_ml;                     // (B Hq, n_splits) reference maximum (log2 units) and sum
+    void *out;                           // (B, Hq, 1, d) contiguous, out_dtype
+    int out_dtype;
+    float *lse;                          // (B, Hq, 1)
+};
+
+int decode_group_splits(int B, int Hkv, int G, long long n_max, bool kv4, int num_sms);
+int launch_decode_group(const DecodeGroupArgs &a, cudaStream_t s);
+
+// Writing and reading a cache held in 4 bits.
+struct Kv4Args {
+    int B, H, T, S, d, dtype;            // T new rows per (b, h); dtype of x (append) or y (read)
+    const void *x[2];                    // K and V rows (append), element strides
+    long long xsB[2], xsH[2], xsT[2];
+    void *y[2];                          // contiguous (B, H, T, d) outputs (read)
+    void *codes[2], *scales[2];          // cache: byte strides
+    long long csB[2], csH[2], csT[2], ssB[2], ssH[2], ssT[2];
+    const int32_t *start;                // (B) first slot, or nullptr = first
+    const int32_t *counts;               // (B) rows to write, or nullptr = T
+    int first;
+    int exp[2];                          // a stored value is code * scale * 2^exp
+};
+
+int launch_kv4_append(const Kv4Args &a, int num_sms, cudaStream_t s);
+int launch_kv4_read(const Kv4Args &a, int num_sms, cudaStream_t s);
 
 // TMA descriptors of Q, K, V (loads) and out (stores, boxes of 32 rows) for
 // the tensor-core kernel.

@@ -282,6 +282,58 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok,
                      void *workspace, size_t workspace_bytes, ba_stream_t stream);
 
 /*
+ * attn_window_fwd -- causal attention with a sliding window and a few first keys
+ * that stay visible (sinks), for prompts and chunks of prompts.  The query at
+ * position p = q_off + i sees the keys j <= p with j > p - window (the window
+ * counts the query's own position) or j < sinks, except padded ones.
+ *  q: (B, Hq, Lq, d) at positions q_off + i; k, v: (B, Hkv, Lk, d) at positions
+ *    0 .. Lk - 1.  Hkv divides Hq: query head h reads key head h / (Hq / Hkv).
+ *    dtype and d as for attn_block_fwd; strides are free (bf16 with d = 64 or 128
+ *    whose strides TMA can read runs on the tensor cores, everything else on the
+ *    CUDA cores in fp32).
+ *  window >= 1, sinks >= 0.
+ *  key_padding_mask: NULL or uint8 (B, >= Lk), 1 = excluded; what K and V hold at
+ *    an excluded key has no effect, infinities and NaN included.
+ *  scale: > 0, or <= 0 for 1/sqrt(d).
+ *  out: (B, Hq, Lq, d) contiguous, 16-byte aligned, out_dtype = BA_F32 or dtype;
+ *    lse: (B, Hq, Lq) fp32.  A row that sees no key gets out = 0, lse = -inf.
+ *  workspace: attn_window_fwd_workspace_size() bytes.
+ * The walk of a query tile is its window and the sinks: the cost is that of
+ * window + sinks keys a row, whatever the length.
+ * Errors: BA_ERR_ARG (NULL pointers, negative sizes, window < 1, a mask that does
+ * not cover Lk keys, a misaligned out), BA_ERR_SHAPE (d, Hq not a multiple of Hkv,
+ * positions of 2^31 and beyond).
+ */
+size_t attn_window_fwd_workspace_size(void);
+int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v,
+                    int B, int Hq, int Hkv, int Lq, int Lk, int d, int dtype,
+                    int64_t q_off, int window, int sinks,
+                    const uint8_t *key_padding_mask, int64_t kpm_ld, float scale,
+                    void *out, int out_dtype, float *lse,
+                    void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
+ * attn_window_bwd -- gradients of attn_window_fwd (the formulas of attn_block_bwd
+ * over the window's pairs); dk and dv of a key head sum over its query heads.
+ *  out, dout: (B, Hq, Lq, d), dtype; lse: the forward's.  Everything else as for
+ *    the forward.  q, out and dout hold finite values.
+ *  dq: (B, Hq, Lq, d); dk, dv: (B, Hkv, Lk, d), contiguous, overwritten, grad_dtype
+ *    = BA_F32 or dtype (sums in fp32, rounded once).
+ *  workspace: attn_window_bwd_workspace_size() bytes: D_i per row, and for the key
+ *    tiles that hold sinks (seen by every later query) fp32 partials over chunks of
+ *    the queries, added in a fixed order.  No atomics: equal calls give equal bits.
+ * Errors: as attn_window_fwd; BA_ERR_SHAPE also for B Hq > 65535.
+ */
+size_t attn_window_bwd_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int d, int64_t q_off,
+                                      int window, int sinks);
+int attn_window_bwd(ba_tensor q, ba_tensor k, ba_tensor v, ba_tensor out, ba_tensor dout, const float *lse,
+                    int B, int Hq, int Hkv, int Lq, int Lk, int d, int dtype,
+                    int64_t q_off, int window, int sinks,
+                    const uint8_t *key_padding_mask, int64_t kpm_ld, float scale,
+                    void *dq, void *dk, void *dv, int grad_dtype,
+                    void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
  * attn_decode_fwd -- decode attention: one query token per (b, h) against a KV
  * cache, split along the keys.  Decode processes one token at a time and
  * shards the KV cache rather than the input tokens ("Sequence/context
@@ -304,6 +356,76 @@ int attn_decode_fwd(ba_tensor q, ba_tensor k_cache, ba_tensor v_cache,
                     const int32_t *lengths, int num_splits, float scale,
                     void *out, int out_dtype, float *lse,
                     void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
+ * attn_window_decode_fwd -- single-token form of attn_window_fwd: sequence b's cache
+ * holds len = lengths[b] keys, its query is at position len - 1 (its own key is in the
+ * cache) and sees the keys [max(0, len - window), len) and [0, min(sinks, len)).
+ *  q: (B, Hq, 1, d); k_cache, v_cache: (B, Hkv, S, d), Hkv dividing Hq, element
+ *    strides, every row on a 16-byte boundary (BA_ERR_ARG otherwise).  Slots behind
+ *    lengths[b] are not read.
+ *  lengths: NULL (S) or device int32[B], clamped to [0, S]; a sequence of length 0
+ *    gets out = 0, lse = -inf.
+ *  out: (B, Hq, 1, d) contiguous, out_dtype BA_F32 or dtype; lse: (B, Hq, 1) fp32.
+ *  workspace: attn_window_decode_workspace_size() bytes (fp32 partials of key splits).
+ * Bound by HBM: each visible K and V byte is read once for all query heads of its
+ * group (up to 16 of them; bf16 with d = 64, 128), whatever S is.
+ * Errors: as attn_window_fwd.
+ */
+size_t attn_window_decode_workspace_size(int B, int Hq, int Hkv, int S, int d, int window, int sinks);
+int attn_window_decode_fwd(ba_tensor q, ba_tensor k_cache, ba_tensor v_cache,
+                           int B, int Hq, int Hkv, int S, int d, int dtype,
+                           const int32_t *lengths, int window, int sinks, float scale,
+                           void *out, int out_dtype, float *lse,
+                           void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
+ * A KV cache held in 4 bits.  Each row of d values (d = 64 or 128) is d / 16 blocks of
+ * sixteen e2m1 codes and one e4m3 scale: value = code * scale * 2^exp with
+ *   scale = e4m3(max |x| 2^-exp / 6),  code = e2m1(x 2^-exp / scale),
+ * rounded to nearest, ties to even, saturating; (d / 2 + d / 16) bytes a row.  Infinities
+ * saturate and NaN is held as the block's largest value.
+ *  codes: (B, H, S, d / 2) bytes, element 2 i of a row in the low half of byte i;
+ *  scales: (B, H, S, d / 16) bytes.  K and V share the BYTE strides given here: codes'
+ *    rows on 16-byte boundaries, scales' on 8-byte ones.
+ *  k_exp, v_exp: the tensors' powers of two, -100 .. 100 (0 suits values whose blocks'
+ *    largest lie in 0.02 .. 2600).
+ */
+typedef struct {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t codes_sB, codes_sH, codes_sT;
+    int64_t scales_sB, scales_sH, scales_sT;
+    int k_exp, v_exp;
+} ba_kv4;
+
+/*
+ * kv4_append -- quantise T new rows of K and V per (b, h) into the cache slots
+ * start[b] + t, t < counts[b].  Slots outside [0, S) are dropped; all others keep what
+ * they hold.
+ *  k, v: (B, H, T, d) of dtype BA_F32 or BA_BF16, strided, rows on 16-byte boundaries.
+ *  start: NULL (0) or device int32[B]; counts: NULL (T) or device int32[B].
+ * kv4_read -- the values of the slots first .. first + T - 1 (0 <= first,
+ * first + T <= S) as contiguous (B, H, T, d) tensors of dtype (bf16 holds them exactly
+ * while they are normal numbers: 6 significant bits).
+ * Errors: BA_ERR_ARG (NULL pointers, misalignment, exponents, a range outside the
+ * cache), BA_ERR_SHAPE (d).
+ */
+int kv4_append(ba_tensor k, ba_tensor v, ba_kv4 cache, int B, int H, int T, int S, int d, int dtype,
+               const int32_t *start, const int32_t *counts, ba_stream_t stream);
+int kv4_read(ba_kv4 cache, int B, int H, int S, int d, int first, int T, int dtype,
+             void *k, void *v, ba_stream_t stream);
+
+/*
+ * attn_decode_kv4_fwd -- single-token attention over a 4-bit cache, as
+ * attn_window_decode_fwd but for the cache and for window = 0, which means every key.
+ *  q: (B, Hq, 1, d) bf16 (BA_ERR_UNSUPPORTED for fp32), rows on 16-byte boundaries.
+ * Bound by HBM: 9/32 of the bf16 cache's bytes.
+ */
+size_t attn_decode_kv4_workspace_size(int B, int Hq, int Hkv, int S, int d, int window, int sinks);
+int attn_decode_kv4_fwd(ba_tensor q, ba_kv4 cache, int B, int Hq, int Hkv, int S, int d, int dtype,
+                        const int32_t *lengths, int window, int sinks, float scale,
+                        void *out, int out_dtype, float *lse,
+                        void *workspace, size_t workspace_bytes, ba_stream_t stream);
 
 /*
  * rope_apply -- rotary position embedding ("RoFormer", item #4 of ai.engineer
