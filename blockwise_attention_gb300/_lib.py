@@ -20,7 +20,8 @@ _ROOT = os.path.dirname(_PKG)
 _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_BUILD, "libblockattn.so")
-_SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu"]
+_SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu",
+            "decode_group.cu", "kv4.cu"]
 _HEADERS = ["common.cuh", "internal.h", "epilogue.cuh", "tc_ptx.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -93,6 +94,13 @@ class ba_tensor(ctypes.Structure):
                 ("sT", ctypes.c_int64)]
 
 
+class ba_kv4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("codes_sB", ctypes.c_int64), ("codes_sH", ctypes.c_int64),
+                ("codes_sT", ctypes.c_int64), ("scales_sB", ctypes.c_int64), ("scales_sH", ctypes.c_int64),
+                ("scales_sT", ctypes.c_int64), ("k_exp", ctypes.c_int), ("v_exp", ctypes.c_int)]
+
+
 EXPORTED = ["attn_block_fwd", "attn_block_fwd_workspace_size", "attn_merge", "ring_attn_fwd",
             "ring_attn_fwd_workspace_size", "rope_apply", "ba_tile_classes", "ba_index_maps",
             "ba_sync_status", "ba_debug_wait_timeout", "ba_strerror", "attn_block_fwd_noalloc",
@@ -100,7 +108,8 @@ EXPORTED = ["attn_block_fwd", "attn_block_fwd_workspace_size", "attn_merge", "ri
             "ulysses_all_to_all", "ulysses_attn_fwd", "ulysses_attn_fwd_workspace_size",
             "attn_decode_fwd", "attn_decode_workspace_size", "ba_pair_schedule",
             "attn_window_fwd", "attn_window_fwd_workspace_size", "attn_window_bwd",
-            "attn_window_bwd_workspace_size"]
+            "attn_window_bwd_workspace_size", "attn_window_decode_fwd", "attn_window_decode_workspace_size",
+            "kv4_append", "kv4_read", "attn_decode_kv4_fwd", "attn_decode_kv4_workspace_size"]
 
 
 def load(path: str | None = None):
@@ -171,6 +180,17 @@ def load(path: str | None = None):
     lib.attn_window_bwd.restype = i
     lib.attn_window_bwd.argtypes = [T, T, T, T, T, vp, i, i, i, i, i, i, i, i64, i, i, vp, i64, f, vp, vp, vp, i,
                                     vp, sz, vp]
+    for fn in (lib.attn_window_decode_workspace_size, lib.attn_decode_kv4_workspace_size):
+        fn.restype = sz
+        fn.argtypes = [i, i, i, i, i, i, i]
+    lib.attn_window_decode_fwd.restype = i
+    lib.attn_window_decode_fwd.argtypes = [T, T, T, i, i, i, i, i, i, vp, i, i, f, vp, i, vp, vp, sz, vp]
+    lib.kv4_append.restype = i
+    lib.kv4_append.argtypes = [T, T, ba_kv4, i, i, i, i, i, i, vp, vp, vp]
+    lib.kv4_read.restype = i
+    lib.kv4_read.argtypes = [ba_kv4, i, i, i, i, i, i, i, vp, vp, vp]
+    lib.attn_decode_kv4_fwd.restype = i
+    lib.attn_decode_kv4_fwd.argtypes = [T, ba_kv4, i, i, i, i, i, i, vp, i, i, f, vp, i, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -615,6 +635,129 @@ def attn_decode_fwd(q, k_cache, v_cache, *, lengths=None, num_splits=0, scale=No
                              _dtype_code(out.dtype), _ptr(lse), _ptr(workspace),
                              0 if workspace is None else workspace.numel(), _stream(stream))
     _check("attn_decode_fwd", rc)
+    return out, lse
+
+
+def _per_sequence(name, t, B, ref):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_cuda or t.numel() != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {B} entries")
+    _like(ref, **{name: t})
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def attn_window_decode_fwd(q, k_cache, v_cache, *, window, sinks=0, lengths=None, scale=None, out=None, out_dtype=None,
+                           lse=None, workspace=None, stream=None):
+    """Single-token form of attn_window_fwd: q (B, Hq, 1, d) at position lengths[b] - 1
+    against the caches (B, Hkv, S, d), Hkv dividing Hq; lengths: int32 (B) or None (S).
+    Returns (out, lse)."""
+    lib = load()
+    Hkv, S = _kv_heads(q, k_cache, v_cache)
+    B, Hq, one, d = q.shape
+    if one != 1:
+        raise ValueError("decode takes one query per (b, h): q of shape (B, Hq, 1, d)")
+    window, sinks = _c_int("window", window, 1), _c_int("sinks", sinks, 0)
+    tq, tk, tv = _tensor(q), _tensor(k_cache), _tensor(v_cache)
+    _like(q, k_cache=k_cache, v_cache=v_cache)
+    lens = _per_sequence("lengths", lengths, B, q)
+    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    need = lib.attn_window_decode_workspace_size(B, Hq, Hkv, S, d, window, sinks)
+    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
+    rc = lib.attn_window_decode_fwd(tq, tk, tv, B, Hq, Hkv, S, d, _dtype_code(q.dtype), lens, window, sinks,
+                                    0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
+                                    ws, ws_bytes, _stream(stream))
+    _check("attn_window_decode_fwd", rc)
+    return out, lse
+
+
+class KV4Cache:
+    """A KV cache held in 4 bits: codes (B, H, S, d / 2) and scales (B, H, S, d / 16), uint8,
+    of K and of V, with the tensors' powers of two; see include/blockattn.h (ba_kv4)."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_exp", "v_exp", "shape", "_c")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_exp=0, v_exp=0):
+        codes, scales = (k_codes, v_codes), (k_scales, v_scales)
+        for t in codes + scales:
+            if t.dtype != torch.uint8 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda or t.device != k_codes.device:
+                raise ValueError("codes and scales are 4-D uint8 CUDA tensors on one device with a contiguous last axis")
+        B, H, S, half = k_codes.shape
+        if half not in (32, 64):
+            raise ValueError(f"codes of {half} bytes a row: rows of d = 64 or 128 values take 32 or 64")
+        if v_codes.shape != k_codes.shape or any(tuple(t.shape) != (B, H, S, half // 8) for t in scales):
+            raise ValueError("codes (B, H, S, d / 2) and scales (B, H, S, d / 16) of K and V must match")
+        if k_codes.stride() != v_codes.stride() or k_scales.stride() != v_scales.stride():
+            raise ValueError("K and V must have the same strides")
+        for e in (k_exp, v_exp):
+            if int(e) != e or not -100 <= e <= 100:
+                raise ValueError(f"exponent {e} is not an integer in [-100, 100]")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_exp, self.v_exp, self.shape = int(k_exp), int(v_exp), (B, H, S, 2 * half)
+        self._c = ba_kv4(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                         *k_codes.stride()[:3], *k_scales.stride()[:3], self.k_exp, self.v_exp)
+
+    @classmethod
+    def empty(cls, B, H, S, d, *, device="cuda", k_exp=0, v_exp=0):
+        """A new cache of S slots per (b, h); its slots hold zeros."""
+        def new(n):
+            return torch.zeros((B, H, S, n), dtype=torch.uint8, device=device)
+        return cls(new(d // 2), new(d // 16), new(d // 2), new(d // 16), k_exp, v_exp)
+
+
+def kv4_append(cache, k, v, *, start=None, counts=None, stream=None):
+    """Quantise k, v (B, H, T, d) into the slots start[b] + t of a KV4Cache (t < counts[b]);
+    start, counts: int32 (B) CUDA tensors or None (0, T).  Slots outside the cache are dropped."""
+    lib = load()
+    B, H, S, d = cache.shape
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[:2] != (B, H) or k.shape[3] != d:
+        raise ValueError(f"k, v of shape {tuple(k.shape)} do not match a cache of {cache.shape}")
+    tk, tv = _tensor(k), _tensor(v)
+    _like(k, v=v, cache=cache.k_codes)
+    rc = lib.kv4_append(tk, tv, cache._c, B, H, k.shape[2], S, d, _dtype_code(k.dtype), _per_sequence("start", start, B, k),
+                        _per_sequence("counts", counts, B, k), _stream(stream))
+    _check("kv4_append", rc)
+    return cache
+
+
+def kv4_read(cache, T, *, first=0, dtype=torch.bfloat16, out_k=None, out_v=None, stream=None):
+    """The values of slots first .. first + T - 1 of a KV4Cache: (k, v), each (B, H, T, d)."""
+    lib = load()
+    B, H, S, d = cache.shape
+    T, first = _c_int("T", T, 0), _c_int("first", first, 0)
+    outs = []
+    for name, t in (("out_k", out_k), ("out_v", out_v)):
+        if t is None:
+            t = _empty((B, H, T, d), dtype, cache.k_codes.device, stream)
+        elif tuple(t.shape) != (B, H, T, d) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(B, H, T, d)}")
+        outs.append(t)
+    _like(cache.k_codes, out_k=outs[0], out_v=outs[1])
+    rc = lib.kv4_read(cache._c, B, H, S, d, first, T, _dtype_code(dtype), _ptr(outs[0]), _ptr(outs[1]), _stream(stream))
+    _check("kv4_read", rc)
+    return outs[0], outs[1]
+
+
+def attn_decode_kv4_fwd(q, cache, *, lengths=None, window=0, sinks=0, scale=None, out=None, out_dtype=None, lse=None,
+                        workspace=None, stream=None):
+    """Single-token attention of q (B, Hq, 1, d) bf16 over a KV4Cache of (B, Hkv, S, d), over
+    every key (window = 0) or a window with sinks; see include/blockattn.h.  Returns (out, lse)."""
+    lib = load()
+    B, Hkv, S, d = cache.shape
+    if q.dim() != 4 or q.shape[0] != B or q.shape[2] != 1 or q.shape[3] != d or Hkv == 0 or q.shape[1] % Hkv:
+        raise ValueError(f"q of shape {tuple(q.shape)} does not match a cache of {cache.shape}")
+    Hq = q.shape[1]
+    window, sinks = _c_int("window", window, 0), _c_int("sinks", sinks, 0)
+    tq = _tensor(q)
+    _like(q, cache=cache.k_codes)
+    lens = _per_sequence("lengths", lengths, B, q)
+    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    need = lib.attn_decode_kv4_workspace_size(B, Hq, Hkv, S, d, window, sinks)
+    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
+    rc = lib.attn_decode_kv4_fwd(tq, cache._c, B, Hq, Hkv, S, d, _dtype_code(q.dtype), lens, window, sinks,
+                                 0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
+                                 ws, ws_bytes, _stream(stream))
+    _check("attn_decode_kv4_fwd", rc)
     return out, lse
 
 

@@ -2032,12 +2032,13 @@ int run_decode_group(ba::DecodeGroupArgs &a, const ba_tensor &q, int B, int Hq, 
     return ba::launch_decode_group(a, stream);
 }
 
-bool kv4_ok(const ba_kv4 &c, int B, int H) {
+bool kv4_ok(const ba_kv4 &c, int B, int H, int d) {
     auto al = [](const void *p, unsigned n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
-    if (!al(c.k_codes, 16) || !al(c.v_codes, 16) || !al(c.k_scales, 8) || !al(c.v_scales, 8)) return false;
-    if (c.codes_sT % 16 || c.scales_sT % 8) return false;
-    if (H > 1 && (c.codes_sH % 16 || c.scales_sH % 8)) return false;
-    if (B > 1 && (c.codes_sB % 16 || c.scales_sB % 8)) return false;
+    const int row = d / 16;   // bytes of a row of scales
+    if (!al(c.k_codes, 16) || !al(c.v_codes, 16) || !al(c.k_scales, row) || !al(c.v_scales, row)) return false;
+    if (c.codes_sT % 16 || c.scales_sT % row) return false;
+    if (H > 1 && (c.codes_sH % 16 || c.scales_sH % row)) return false;
+    if (B > 1 && (c.codes_sB % 16 || c.scales_sB % row)) return false;
     return c.k_exp >= -100 && c.k_exp <= 100 && c.v_exp >= -100 && c.v_exp <= 100;
 }
 
@@ -2113,7 +2114,7 @@ int attn_decode_kv4_fwd(ba_tensor q, ba_kv4 cache, int B, int Hq, int Hkv, int S
     if (dtype != BA_BF16) return BA_ERR_UNSUPPORTED;
     if (d != 64 && d != 128) return BA_ERR_SHAPE;
     if ((long long)B * Hq == 0) return BA_OK;
-    if (check_tensor(q) || !out || !lse || (S > 0 && !kv4_ok(cache, B, Hkv))) return BA_ERR_ARG;
+    if (check_tensor(q) || !out || !lse || (S > 0 && !kv4_ok(cache, B, Hkv, d))) return BA_ERR_ARG;
     q = fix_unit_strides(q, B, Hq, 1, d);
     if (!rows16(q.ptr, B > 1 ? q.sB : 0, Hq > 1 ? q.sH : 0, d, 2)) return BA_ERR_ARG;
     const int dev = current_device();
@@ -2142,7 +2143,7 @@ int kv4_append(ba_tensor k, ba_tensor v, ba_kv4 cache, int B, int H, int T, int 
     if (B < 0 || H < 0 || T < 0 || S < 0 || !valid_dtype(dtype)) return BA_ERR_ARG;
     if (d != 64 && d != 128) return BA_ERR_SHAPE;
     if ((long long)B * H * T == 0 || S == 0) return BA_OK;
-    if (!kv4_ok(cache, B, H)) return BA_ERR_ARG;
+    if (!kv4_ok(cache, B, H, d)) return BA_ERR_ARG;
     const size_t eb = elem_size(dtype);
     ba::Kv4Args a;
     std::memset(&a, 0, sizeof a);
@@ -2177,7 +2178,7 @@ int kv4_read(ba_kv4 cache, int B, int H, int S, int d, int first, int T, int dty
         return BA_ERR_ARG;
     if (d != 64 && d != 128) return BA_ERR_SHAPE;
     if ((long long)B * H * T == 0) return BA_OK;
-    if (!kv4_ok(cache, B, H) || !k || !v) return BA_ERR_ARG;
+    if (!kv4_ok(cache, B, H, d) || !k || !v) return BA_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(k) % 16 || reinterpret_cast<uintptr_t>(v) % 16) return BA_ERR_ARG;
     const int dev = current_device();
     if (dev < 0) return BA_ERR_CUDA;

@@ -387,7 +387,7 @@ int attn_window_decode_fwd(ba_tensor q, ba_tensor k_cache, ba_tensor v_cache,
  * saturate and NaN is held as the block's largest value.
  *  codes: (B, H, S, d / 2) bytes, element 2 i of a row in the low half of byte i;
  *  scales: (B, H, S, d / 16) bytes.  K and V share the BYTE strides given here: codes'
- *    rows on 16-byte boundaries, scales' on 8-byte ones.
+ *    rows on 16-byte boundaries, scales' on d / 16-byte ones.
  *  k_exp, v_exp: the tensors' powers of two, -100 .. 100 (0 suits values whose blocks'
  *    largest lie in 0.02 .. 2600).
  */

@@ -49,13 +49,15 @@ def score_error(q, k, scale=None):
     return float(d * 2.0 ** -24 * big * sc)
 
 
-def check_forward(out, lse, q, k, v, seen, scale=None, label=""):
-    """fp32 kernels: the scores' error e moves every p by a factor in 1 +- (e + 2^-20)
+def check_forward(out, lse, q, k, v, seen, scale=None, label="", p_step=None):
+    """p_step: the rounding of p before P V where it is not that of q's type.  fp32 kernels: the scores' error e moves every p by a factor in 1 +- (e + 2^-20)
     (the exponential, the running sums).  bf16 kernels round p once to bf16 before
     P V.  Then one rounding to out's type."""
     o, l, p, pa = forward(q, k, v, seen, scale)
     e = 2.0 * score_error(q, k, scale) + 2.0 ** -20
-    rel_p = e + (HALF_STEP[torch.bfloat16] if q.dtype == torch.bfloat16 else 0.0)
+    if p_step is None:
+        p_step = HALF_STEP[torch.bfloat16] if q.dtype == torch.bfloat16 else 0.0
+    rel_p = e + p_step
     tol = rel_p * pa * 1.01 + HALF_STEP[out.dtype] * (o.abs() + rel_p * pa) + 1e-30
     bad = (out.double() - o).abs() > tol
     assert torch.isfinite(out).all(), f"{label}: non-finite out"
@@ -99,3 +101,13 @@ def check_backward(grads, q, k, v, out, dout, lse, seen, scale=None, label=""):
         tol = tol + HALF_STEP[got.dtype] * (ref.abs() + tol) + 1e-30
         err = (got.double() - ref).abs()
         assert (err <= tol).all(), (label, name, float((err - tol).max()), float(err.max()), int((err > tol).sum()))
+
+
+def visible_decode(lengths, S, window, sinks, device):
+    """(B, 1, 1, S) bool: the slots that the newest token of each sequence sees."""
+    n = lengths.long().clamp(0, S)[:, None]
+    j = torch.arange(S, device=device)[None, :]
+    m = j < n
+    if window > 0:
+        m = m & ((j >= n - window) | (j < sinks))
+    return m[:, None, None]
