@@ -9,5 +9,6 @@ from ._lib import (  # noqa: F401
     attn_block_bwd, attn_block_fwd, attn_decode_fwd, attn_block_fwd_noalloc, attn_merge, build, debug_wait_timeout, index_maps, load,
     pair_schedule, ring_attn_bwd, ring_attn_fwd, ring_attn_fwd_workspace_size, rope_apply, sync_status, tile_classes,
     ulysses_all_to_all, ulysses_attn_fwd, attn_window_bwd, attn_window_fwd, attn_window_decode_fwd,
-    KV4Cache, kv4_append, kv4_read, attn_decode_kv4_fwd,
+    KV4Cache, kv4_append, kv4_read, attn_decode_kv4_fwd, qk_norm_rope_bwd,
+    qk_norm_rope_fwd,
 )

@@ -21,7 +21,7 @@ _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_BUILD, "libblockattn.so")
 _SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu",
-            "decode_group.cu", "kv4.cu"]
+            "decode_group.cu", "kv4.cu", "qk_norm.cu"]
 _HEADERS = ["common.cuh", "internal.h", "epilogue.cuh", "tc_ptx.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -109,7 +109,8 @@ EXPORTED = ["attn_block_fwd", "attn_block_fwd_workspace_size", "attn_merge", "ri
             "attn_decode_fwd", "attn_decode_workspace_size", "ba_pair_schedule",
             "attn_window_fwd", "attn_window_fwd_workspace_size", "attn_window_bwd",
             "attn_window_bwd_workspace_size", "attn_window_decode_fwd", "attn_window_decode_workspace_size",
-            "kv4_append", "kv4_read", "attn_decode_kv4_fwd", "attn_decode_kv4_workspace_size"]
+            "kv4_append", "kv4_read", "attn_decode_kv4_fwd", "attn_decode_kv4_workspace_size",
+            "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size"]
 
 
 def load(path: str | None = None):
@@ -191,6 +192,13 @@ def load(path: str | None = None):
     lib.kv4_read.argtypes = [ba_kv4, i, i, i, i, i, i, i, vp, vp, vp]
     lib.attn_decode_kv4_fwd.restype = i
     lib.attn_decode_kv4_fwd.argtypes = [T, ba_kv4, i, i, i, i, i, i, vp, i, i, f, vp, i, vp, vp, sz, vp]
+    lib.qk_norm_rope_fwd.restype = i
+    lib.qk_norm_rope_fwd.argtypes = [T, T, vp, vp, i, i, i, i, i, i, i, f, vp, i64, f, f, vp, vp, vp]
+    lib.qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.qk_norm_rope_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.qk_norm_rope_bwd.restype = i
+    lib.qk_norm_rope_bwd.argtypes = [T, T, vp, vp, i, T, T, i, i, i, i, i, i, i, f, vp, i64, f, f, vp, vp, vp, vp, vp, sz,
+                                     vp]
     _lib = lib
     return lib
 
@@ -780,6 +788,82 @@ def rope_apply(x, *, x2=None, base=10000.0, positions=None, pos_scale=1.0, out=N
     _check("rope_apply", lib.rope_apply(_tensor(x), t2, B, H, T, d, _dtype_code(x.dtype), _ptr(positions),
                                         float(base), float(pos_scale), _ptr(out), _ptr(out2), _stream(stream)))
     return out if x2 is None else (out, out2)
+
+
+def _norm_inputs(q, k, wq, wk, positions):
+    """Checks of qk_norm_rope_*: ((B, Hq, Hkv, T, d), weight dtype code, positions pointer, ld)."""
+    B, Hq, T, d = q.shape
+    if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
+        raise ValueError(f"k of shape {tuple(k.shape)} does not match q of shape {tuple(q.shape)}")
+    if k.dtype != q.dtype or wq.dtype != wk.dtype or wq.dtype not in (q.dtype, torch.float32):
+        raise TypeError("q and k share a dtype; the weights have it too or are float32")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if tuple(w.shape) != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {d} entries")
+    _like(q, k=k, wq=wq, wk=wk, positions=positions)
+    ld = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T or \
+                (T > 1 and positions.stride(-1) != 1) or (positions.dim() == 2 and positions.shape[0] not in (1, B)):
+            raise ValueError(f"positions must be an int32 CUDA tensor (T,) or (B, T) with T = {T}")
+        if positions.dim() == 2 and positions.shape[0] == B and B > 1:
+            ld = positions.stride(0)
+            if ld < T:   # (an expanded row is shared by all)
+                if ld != 0:
+                    raise ValueError("the rows of positions overlap")
+    return (B, Hq, k.shape[1], T, d), _dtype_code(wq.dtype), _ptr(positions), ld
+
+
+def qk_norm_rope_fwd(q, k, wq, wk, *, eps=1e-6, positions=None, base=10000.0, pos_scale=1.0, out_q=None, out_k=None,
+                     stream=None):
+    """Per-head RMS norm and rotation of q (B, Hq, T, d) and k (B, Hkv, T, d) in one pass;
+    wq, wk (d); positions: int32 (T,) or (B, T), None: 0 .. T - 1; see include/blockattn.h.
+    Returns (yq, yk), contiguous."""
+    lib = load()
+    tq, tk = _tensor(q), _tensor(k)
+    sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
+    outs = []
+    for name, y, x in (("out_q", out_q, q), ("out_k", out_k, k)):
+        if y is None:
+            y = _empty(x.shape, q.dtype, q.device, stream)
+        elif y.shape != x.shape or y.dtype != q.dtype or not y.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor of shape {tuple(x.shape)}")
+        outs.append(y)
+    _like(q, out_q=outs[0], out_k=outs[1])
+    rc = lib.qk_norm_rope_fwd(tq, tk, _ptr(wq), _ptr(wk), wdt, *sizes, _dtype_code(q.dtype), float(eps), pos, ld,
+                              float(base), float(pos_scale), _ptr(outs[0]), _ptr(outs[1]), _stream(stream))
+    _check("qk_norm_rope_fwd", rc)
+    return outs[0], outs[1]
+
+
+def qk_norm_rope_bwd(q, k, wq, wk, dyq, dyk, *, eps=1e-6, positions=None, base=10000.0, pos_scale=1.0, dq=None, dk=None,
+                     workspace=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of qk_norm_rope_fwd for dyq, dyk (of q's dtype or
+    float32): dq, dk of q's dtype, dwq, dwk float32."""
+    lib = load()
+    tq, tk, tgq, tgk = _tensor(q), _tensor(k), _tensor(dyq), _tensor(dyk)
+    sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
+    if dyq.shape != q.shape or dyk.shape != k.shape:
+        raise ValueError("dyq and dyk must have the shapes of q and k")
+    if dyq.dtype != dyk.dtype or dyq.dtype not in (q.dtype, torch.float32):
+        raise TypeError("dyq and dyk have the dtype of q or are float32")
+    grads = []
+    for name, t, x in (("dq", dq, q), ("dk", dk, k)):
+        if t is None:
+            t = _empty(x.shape, q.dtype, q.device, stream)
+        elif t.shape != x.shape or t.dtype != q.dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor of shape {tuple(x.shape)}")
+        grads.append(t)
+    _like(q, dyq=dyq, dyk=dyk, dq=grads[0], dk=grads[1])
+    d = sizes[4]
+    dw = _empty((2, d), torch.float32, q.device, stream)
+    ws, ws_bytes, keep = _scratch(lib.qk_norm_rope_bwd_workspace_size(*sizes, _dtype_code(q.dtype)), workspace, q.device,
+                                  stream)
+    rc = lib.qk_norm_rope_bwd(tq, tk, _ptr(wq), _ptr(wk), wdt, tgq, tgk, _dtype_code(dyq.dtype), *sizes,
+                              _dtype_code(q.dtype), float(eps), pos, ld, float(base), float(pos_scale), _ptr(grads[0]),
+                              _ptr(grads[1]), _ptr(dw[0]), _ptr(dw[1]), ws, ws_bytes, _stream(stream))
+    _check("qk_norm_rope_bwd", rc)
+    return grads[0], grads[1], dw[0], dw[1]
 
 
 def tile_classes(B, Lq, Lk, *, q_off=0, k_off=0, key_padding_mask=None, attn_mask=None, causal=False,

@@ -961,6 +961,11 @@ int run_attention(AttnArgs &a, int dev, int nrows_q, int nrows_k, cudaStream_t s
     return launch_attn_tc(a, m, g_num_sms[dev], s);
 }
 
+bool rows16(const void *p, long long sB, long long sH, long long sT, size_t eb) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (sB * (long long)eb) % 16 == 0 &&
+           (sH * (long long)eb) % 16 == 0 && (sT * (long long)eb) % 16 == 0;
+}
+
 int check_tensor(const ba_tensor &t) { return t.ptr ? BA_OK : BA_ERR_ARG; }
 
 }  // namespace
@@ -1651,6 +1656,134 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok, in
 }
 
 // ---------------------------------------------------------------------------
+// Norm per head and rotation of queries and keys
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Checks what the forward and the backward share and fills it in; BA_OK with
+// a.places = 0 when there is nothing to do.
+int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype, int B, int Hq,
+                 int Hkv, int T, int d, int dtype, float eps, const int32_t *positions, int64_t positions_ld, float base,
+                 float pos_scale, void *yq, void *yk, bool &vec) {
+    std::memset(&a, 0, sizeof a);
+    if (B < 0 || Hq < 0 || Hkv < 0 || T < 0 || !valid_dtype(dtype) || !(eps >= 0.f) || !(base > 0.f) ||
+        !(pos_scale >= 0.f) || positions_ld < 0)
+        return BA_ERR_ARG;
+    if (w_dtype != BA_F32 && w_dtype != dtype) return BA_ERR_ARG;
+    if (!valid_d(d)) return BA_ERR_SHAPE;
+    if ((long long)B * ((long long)Hq + Hkv) > 0x7fffffffLL - 64) return BA_ERR_SHAPE;
+    if ((long long)B * ((long long)Hq + Hkv) * T == 0) return BA_OK;
+    const ba_tensor x[2] = {q, k};
+    const void *w[2] = {wq, wk};
+    void *y[2] = {yq, yk};
+    const int H[2] = {Hq, Hkv};
+    const size_t eb = elem_size(dtype);
+    vec = true;
+    for (int i = 0; i < 2; ++i) {
+        a.H[i] = H[i];
+        if (H[i] == 0) continue;
+        if (check_tensor(x[i]) || !w[i] || !y[i]) return BA_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(y[i]) % 16) return BA_ERR_ARG;   // outputs are stored in 16-byte vectors
+        a.x[i] = x[i].ptr;
+        a.sB[i] = x[i].sB;
+        a.sH[i] = x[i].sH;
+        a.sT[i] = x[i].sT;
+        a.w[i] = w[i];
+        a.y[i] = y[i];
+        vec = vec && rows16(x[i].ptr, B > 1 ? x[i].sB : 0, H[i] > 1 ? x[i].sH : 0, T > 1 ? x[i].sT : 0, eb);
+    }
+    a.B = B;
+    a.T = T;
+    a.d = d;
+    a.dtype = dtype;
+    a.w_f32 = w_dtype == BA_F32;
+    a.eps = eps;
+    a.positions = positions;
+    a.pos_ld = positions_ld;
+    a.pos_scale = pos_scale > 0.f ? (double)pos_scale : 1.0;
+    for (int c = 0; c < d / 2; ++c)
+        a.turn[c] = std::pow((double)base, -(double)(2 * c) / (double)d) / 6.283185307179586476925286766559;
+    const bool own = positions && positions_ld > 0;   // each sequence has its own positions
+    a.places = own ? (long long)B * T : T;
+    a.nb = own ? 1 : B;
+    return BA_OK;
+}
+
+size_t qk_norm_bytes(int B, int Hq, int Hkv, int T, int d, int dtype, bool own, int num_sms) {
+    int gx, gy;
+    ba::qk_norm_grid(own ? (long long)B * T : T, (own ? 1 : B) * (Hq + Hkv), d, dtype, num_sms, gx, gy);
+    return align256((size_t)gx * gy * 2 * d * 4);
+}
+
+}  // namespace
+
+int qk_norm_rope_fwd(ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype, int B, int Hq, int Hkv, int T,
+                     int d, int dtype, float eps, const int32_t *positions, int64_t positions_ld, float base,
+                     float pos_scale, void *yq, void *yk, ba_stream_t stream) {
+    ba::QkNormArgs a;
+    bool vec;
+    int rc = qk_norm_args(a, q, k, wq, wk, w_dtype, B, Hq, Hkv, T, d, dtype, eps, positions, positions_ld, base, pos_scale,
+                          yq, yk, vec);
+    if (rc || a.places == 0) return rc;
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    return ba::launch_qk_norm(a, false, BA_F32, vec, g_num_sms[dev], nullptr, nullptr, stream);
+}
+
+size_t qk_norm_rope_bwd_workspace_size(int B, int Hq, int Hkv, int T, int d, int dtype) {
+    if (B < 0 || Hq < 0 || Hkv < 0 || T < 0 || !valid_d(d) || !valid_dtype(dtype)) return 0;
+    const int dev = current_device();
+    const int sms = dev >= 0 && g_num_sms[dev] > 0 ? g_num_sms[dev] : 152;
+    size_t need = 0;
+    for (int own = 0; own < 2; ++own)   // whatever the positions, and before the device is known
+        for (int n : {sms, 152}) {
+            const size_t x = qk_norm_bytes(B, Hq, Hkv, T, d, dtype, own != 0, n);
+            if (x > need) need = x;
+        }
+    return need;
+}
+
+int qk_norm_rope_bwd(ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype, ba_tensor dyq, ba_tensor dyk,
+                     int dy_dtype, int B, int Hq, int Hkv, int T, int d, int dtype, float eps, const int32_t *positions,
+                     int64_t positions_ld, float base, float pos_scale, void *dq, void *dk, float *dwq, float *dwk,
+                     void *workspace, size_t workspace_bytes, ba_stream_t stream) {
+    ba::QkNormArgs a;
+    bool vec;
+    if (dy_dtype != BA_F32 && dy_dtype != dtype) return BA_ERR_ARG;
+    if ((Hq > 0 && !dwq) || (Hkv > 0 && !dwk)) return BA_ERR_ARG;
+    int rc = qk_norm_args(a, q, k, wq, wk, w_dtype, B, Hq, Hkv, T, d, dtype, eps, positions, positions_ld, base, pos_scale,
+                          dq, dk, vec);
+    if (rc) return rc;
+    if (a.places == 0) {   // no rows: the weights' gradients are zero
+        if ((dwq && cudaMemsetAsync(dwq, 0, (size_t)d * 4, stream) != cudaSuccess) ||
+            (dwk && cudaMemsetAsync(dwk, 0, (size_t)d * 4, stream) != cudaSuccess))
+            return BA_ERR_CUDA;
+        return BA_OK;
+    }
+    const ba_tensor g[2] = {dyq, dyk};
+    for (int i = 0; i < 2; ++i) {
+        if (a.H[i] == 0) continue;
+        if (check_tensor(g[i])) return BA_ERR_ARG;
+        a.g[i] = g[i].ptr;
+        a.gB[i] = g[i].sB;
+        a.gH[i] = g[i].sH;
+        a.gT[i] = g[i].sT;
+        vec = vec && rows16(g[i].ptr, B > 1 ? g[i].sB : 0, a.H[i] > 1 ? g[i].sH : 0, T > 1 ? g[i].sT : 0,
+                            elem_size(dy_dtype));
+    }
+    const int dev = current_device();
+    if (dev < 0) return BA_ERR_CUDA;
+    if ((rc = device_setup(dev))) return rc;
+    Scratch ws;
+    const size_t need = qk_norm_bytes(B, Hq, Hkv, T, d, dtype, a.nb == 1 && a.places != T, g_num_sms[dev]);
+    if ((rc = ws.acquire(workspace, workspace_bytes, need, stream))) return rc;
+    a.part = static_cast<float *>(ws.ptr);
+    return ba::launch_qk_norm(a, true, dy_dtype, vec, g_num_sms[dev], dwq, dwk, stream);
+}
+
+// ---------------------------------------------------------------------------
 // Sliding window with sinks
 // ---------------------------------------------------------------------------
 
@@ -1889,11 +2022,6 @@ int decode_splits(int B, int H, int S, int num_splits, int num_sms) {
     if (n > cap) n = cap;
     if (n < 1) n = 1;
     return (int)n;
-}
-
-bool rows16(const void *p, long long sB, long long sH, long long sT, size_t eb) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (sB * (long long)eb) % 16 == 0 &&
-           (sH * (long long)eb) % 16 == 0 && (sT * (long long)eb) % 16 == 0;
 }
 
 }  // namespace

@@ -153,6 +153,28 @@ struct Kv4Args {
 int launch_kv4_append(const Kv4Args &a, int num_sms, cudaStream_t s);
 int launch_kv4_read(const Kv4Args &a, int num_sms, cudaStream_t s);
 
+// Norm per head and rotation of queries ([0]) and keys ([1]), forward or backward.
+struct QkNormArgs {
+    int B, T, d, dtype, H[2];
+    const void *x[2], *w[2];
+    long long sB[2], sH[2], sT[2];       // element strides of x
+    const void *g[2];                    // dy (backward)
+    long long gB[2], gH[2], gT[2];
+    int w_f32;                           // weights fp32 (else dtype)
+    void *y[2];                          // y, or dx: contiguous (B, H, T, d)
+    const int32_t *positions;            // nullptr: t
+    long long pos_ld;                    // entries between sequences (0: shared)
+    double pos_scale, turn[64];          // turn[c] = base^(-2c/d) / (2 pi)
+    float eps;
+    long long places;                    // T, or B T when each sequence has its own positions
+    int nb;                              // sequences of a place: B, or 1
+    float *part;                         // backward: (blocks, 2, d) sums of dz n
+};
+
+void qk_norm_grid(long long places, int rows, int d, int dtype, int num_sms, int &gx, int &gy);
+int launch_qk_norm(const QkNormArgs &a, bool bwd, int g_dtype, bool vec, int num_sms, float *dwq, float *dwk,
+                   cudaStream_t s);
+
 // TMA descriptors of Q, K, V (loads) and out (stores, boxes of 32 rows) for
 // the tensor-core kernel.
 struct TmaMaps {

@@ -451,6 +451,37 @@ int rope_apply(ba_tensor x, ba_tensor x2, int B, int H, int T, int d, int dtype,
                ba_stream_t stream);
 
 /*
+ * qk_norm_rope_fwd -- per-head RMS norm of queries and keys and their rotation in one
+ * pass: for each row x (d values of one head at position m)
+ *   z = x / sqrt(mean(x^2) + eps) * w,  y = the rotation of rope_apply of z at m.
+ *  q: (B, Hq, T, d), k: (B, Hkv, T, d), dtype, any strides (16-byte aligned rows are
+ *    read in vectors); either head count may be 0 (its pointers are then not used).
+ *    d: 16, 32, 64 or 128.
+ *  wq, wk: (d) weights, w_dtype = BA_F32 or dtype.  eps >= 0.
+ *  positions: NULL (position of row t is t), or device int32: entry (b, t) at
+ *    positions[b * positions_ld + t]; positions_ld = 0: one row shared by all sequences.
+ *  base, pos_scale: as for rope_apply.
+ *  yq: (B, Hq, T, d), yk: (B, Hkv, T, d): contiguous, 16-byte aligned, dtype; computed
+ *    in fp32 (the angles in fp64) and rounded once.
+ * qk_norm_rope_bwd -- the gradients for dyq, dyk (shapes of q and k, strided, dy_dtype =
+ *  BA_F32 or dtype): dq, dk contiguous of dtype; dwq, dwk (d) fp32, summed over all
+ *  rows in a fixed order.  workspace: qk_norm_rope_bwd_workspace_size() bytes.
+ * Errors: BA_ERR_ARG (NULL pointers, negative sizes, eps or pos_scale, base <= 0, NaN, a
+ * misaligned output), BA_ERR_SHAPE (d).
+ */
+int qk_norm_rope_fwd(ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype,
+                     int B, int Hq, int Hkv, int T, int d, int dtype, float eps,
+                     const int32_t *positions, int64_t positions_ld, float base, float pos_scale,
+                     void *yq, void *yk, ba_stream_t stream);
+size_t qk_norm_rope_bwd_workspace_size(int B, int Hq, int Hkv, int T, int d, int dtype);
+int qk_norm_rope_bwd(ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype,
+                     ba_tensor dyq, ba_tensor dyk, int dy_dtype,
+                     int B, int Hq, int Hkv, int T, int d, int dtype, float eps,
+                     const int32_t *positions, int64_t positions_ld, float base, float pos_scale,
+                     void *dq, void *dk, float *dwq, float *dwk,
+                     void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
  * ba_tile_classes -- class of each 128 x 128 tile of the combined exclusion
  * mask for the block rows [q_off, q_off+Lq) x keys [k_off, k_off+Lk), tiles
  * counted from the block origin: BA_TILE_EMPTY (no visible pair), FULL (all
