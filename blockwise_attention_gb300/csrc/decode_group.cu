@@ -13,17 +13,21 @@
 // decode_mma_kernel (bf16 cache with d = 64, 128; 4-bit cache).  What bounds it is HBM:
 //   a key costs 4 G d flop for 4 d bytes (bf16) or 1.125 d bytes (4 bits), G <= 16.  On
 //   the CUDA cores that would be 2 G d FMAs a key, beyond the fp32 rate from about G = 4
-//   at 6.8 TB/s; the products therefore run as mma.sync m16n8k16 with the query heads as
-//   M.  (tcgen05.mma needs 128 rows of M or N and its operands in shared memory in its
-//   own layout, which for the 4-bit cache would mean writing every unpacked value back
-//   to shared memory; here the fragments are unpacked in the registers that loaded
-//   them.)  A warp works alone on tiles of 16 keys, which it brings in with cp.async
-//   through a ring of its own in shared memory: every lane copies exactly the bytes that
-//   it will use and reads them back itself, so the loop has no block barrier.
-//   Fragments: the order of d inside the contraction q . k and that of the columns of O
-//   are free, so a lane (g = lane / 4, t = lane % 4) takes contiguous runs: of key g the
-//   d's of t for K, and of the keys 2t, 2t+1, 2t+8, 2t+9 the d's of g for V; the pairs of
-//   keys that the P V fragment wants side by side are put together with byte permutes.
+//   at 6.8 TB/s; the products therefore run as mma.sync m16n8k16.  (tcgen05.mma needs its
+//   operands in shared memory in its own layout, which for the 4-bit cache would mean
+//   writing every unpacked value back to shared memory; here the fragments are unpacked in
+//   the registers that loaded them.)  The keys are M of S^T = K q^T, the d's M of O^T =
+//   V^T P^T, eight query heads N: no row of a fragment is empty at G = 8, and O takes half
+//   the registers that it takes with the heads as M.  P passes from one product to the
+//   other by two 8 x 8 transposes a tile.
+//   A warp works alone on tiles of 16 keys, which it brings in with cp.async through a
+//   ring of its own in shared memory: every lane copies exactly the bytes that it will use
+//   and reads them back itself, so the loop has no block barrier.
+//   Fragments: the order of d inside the contraction q . k and that of the rows of O^T are
+//   free, so a lane (g = lane / 4, t = lane % 4) takes contiguous runs: of the keys g and
+//   g + 8 the d's of t for K, and of the keys 2t, 2t+1, 2t+8, 2t+9 the d's of g for V; the
+//   pairs of keys that V^T's fragment wants side by side are put together with byte
+//   permutes (bf16), or by joining two keys' nibbles before the conversion (4 bits).
 //   4 bits: a code times its e4m3 scale has 6 significant bits, so the unpacked values are
 //   exact in fp16; q is scaled by a power of two to at most 2 in magnitude before its
 //   conversion (bf16 values keep their 8 bits down to 2^-14 of the largest), and p is
@@ -151,6 +155,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
     return o;
 }
+// An 8 x 8 matrix of 16-bit values across the warp (lane (g, t): row g, columns 2t, 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -175,24 +185,27 @@ __device__ __forceinline__ void store_split(const DecodeGroupArgs &a, int b, int
     if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (ref + log2f(L)) * LN2;
 }
 
-// One stage of a warp's ring: a tile of 16 keys, in the order in which the lanes read it.
+// One stage of a warp's ring: SUB tiles of 16 keys, in the order in which the lanes read
+// them.  bf16: K of a tile as [key half][chunk of 32 d's][lane], V as [key 0..3 of the
+// lane][chunk of 64 d's][lane], 16 bytes each.  4 bits: K as [key half][lane] (D / 8
+// bytes), V as [key 0..3][lane] (D / 16 bytes); then the stage's scales, K's and V's, key by key.
 template <int D, bool KV4>
 struct Ring {
-    // bf16: K as [key half][chunk of 32 d's][lane] and V as [key 0..3 of the lane][chunk of 64 d's][lane], 16 bytes each.
-    // 4 bits: K as [key half][lane] (D / 8 bytes), V as [key 0..3][lane] (D / 16 bytes), then the 16 keys' scales of K and V.
+    static constexpr int SUB = KV4 ? 2 : 1, KEYS = 16 * SUB;
     static constexpr int K_BYTES = KV4 ? 2 * 32 * (D / 8) : 2 * (D / 32) * 512;
     static constexpr int V_BYTES = KV4 ? 4 * 32 * (D / 16) : 4 * (D / 64) * 512;
-    static constexpr int SC_ROW = D / 16;
-    static constexpr int SC_BYTES = KV4 ? 2 * 16 * SC_ROW : 0;
-    static constexpr int STAGE = K_BYTES + V_BYTES + SC_BYTES;
-    static constexpr int NS = KV4 ? 6 : 3;
+    static constexpr int TILE16 = K_BYTES + V_BYTES;
+    static constexpr int SC_ROW = D / 16, SC_OFF = SUB * TILE16;
+    static constexpr int STAGE = SC_OFF + (KV4 ? 2 * KEYS * SC_ROW : 0);
+    static constexpr int NS = 3;
     static constexpr int BYTES = DG_WARPS * NS * STAGE;
 };
 
-template <int D, bool KV4, int HALVES>
+// NH: groups of 8 query heads (G <= 8 NH).
+template <int D, bool KV4, int NH>
 __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeGroupArgs a) {
     using R = Ring<D, KV4>;
-    constexpr int NT = D / 8;    // column tiles of O
+    constexpr int MT = D / 16;   // row tiles of O^T
     constexpr int KS = D / 16;   // steps of the contraction over d
     extern __shared__ __align__(128) uint8_t dg_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -202,91 +215,85 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
     const int v0 = split * a.split_len, v1 = min(kr.n, v0 + a.split_len);
     if (v0 >= v1 && a.n_splits > 1) return;   // the join reads the splits that hold keys
 
-    // q fragments: the d's that lane t contracts, in the order of its K words.  4 bits:
-    // times a power of two that brings the row's largest magnitude into [1, 2).
-    uint32_t qa[KS][2 * HALVES];   // [step][2 half + k half]
-    float sl2[2] = {a.scale_log2, a.scale_log2};
-#pragma unroll
-    for (int hf = 0; hf < HALVES; ++hf) {
-        const int row = g + 8 * hf;
-        uint32_t w[2 * KS];
-        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (long long)b * a.qsB +
-                                  (long long)(hk * a.G + h0 + min(row, nh - 1)) * a.qsH;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            const int d0 = KV4 ? t * (D / 4) + c * 8 : c * 32 + t * 8;
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(qp + d0));
-            w[4 * c] = u.x;
-            w[4 * c + 1] = u.y;
-            w[4 * c + 2] = u.z;
-            w[4 * c + 3] = u.w;
-        }
-        if constexpr (KV4) {
-            uint32_t big = 0;   // largest magnitude, as bits
-#pragma unroll
-            for (int i = 0; i < 2 * KS; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const int e = min(max((int)(big >> 7), 1), 253);   // biased exponent
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
-            sl2[hf] *= up;
-#pragma unroll
-            for (int i = 0; i < 2 * KS; ++i)
-                w[i] = pack16(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down, true);
-        }
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qa[s][2 * hf] = row < nh ? w[2 * s] : 0u;
-            qa[s][2 * hf + 1] = row < nh ? w[2 * s + 1] : 0u;
-        }
-    }
-
     const uint32_t ring = smem_u32(dg_smem) + (uint32_t)warp * R::NS * R::STAGE;
     const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH;
     const uint8_t *vb = static_cast<const uint8_t *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH;
     const uint8_t *ksb = KV4 ? static_cast<const uint8_t *>(a.k_scales) + (long long)b * a.kcB + (long long)hk * a.kcH : nullptr;
     const uint8_t *vsb = KV4 ? static_cast<const uint8_t *>(a.v_scales) + (long long)b * a.vcB + (long long)hk * a.vcH : nullptr;
 
-    // Tile i of this warp: indices v0 + 16 (warp + DG_WARPS i) ..; keys behind v1 are
+    // Stage i of this warp: indices v0 + KEYS (warp + DG_WARPS i) ..; keys behind v1 are
     // not read (their bytes arrive as zeros).
-    const int tiles = v1 > v0 ? (v1 - v0 + 15) / 16 : 0;
-    const int mine = tiles > warp ? (tiles - warp + DG_WARPS - 1) / DG_WARPS : 0;
+    const int stages = v1 > v0 ? (v1 - v0 + R::KEYS - 1) / R::KEYS : 0;
+    const int mine = stages > warp ? (stages - warp + DG_WARPS - 1) / DG_WARPS : 0;
+    // the lane's part of a key's row: its bytes from row + k_part (v_part) on
+    const int k_part = KV4 ? t * (D / 8) : t * 16, v_part = KV4 ? g * (D / 16) : g * 16;
+    const long long k_lane = g * a.ksT + k_part, k8 = 8 * a.ksT, v_lane = 2 * t * a.vsT + v_part, v8 = 8 * a.vsT;
+    const long long ks_lane = lane * a.kcT, vs_lane = lane * a.vcT;
+    auto copy_k = [&](uint32_t dst, const uint8_t *at, bool in) {
+        if constexpr (KV4 && D == 128)
+            cp16(dst + lane * 16, at, in);
+        else if constexpr (KV4)
+            cp_small<8>(dst + lane * 8, at, in);
+        else
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) cp16(dst + (c * 32 + lane) * 16, at + c * 64, in);
+    };
+    auto copy_v = [&](uint32_t dst, const uint8_t *at, bool in) {
+        if constexpr (KV4)
+            cp_small<D / 16>(dst + lane * (D / 16), at, in);
+        else
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) cp16(dst + (c * 32 + lane) * 16, at + c * 128, in);
+    };
     auto issue = [&](int i) {
         if (i < mine) {
             const uint32_t st = ring + (uint32_t)(i % R::NS) * R::STAGE;
-            const int i0 = v0 + 16 * (warp + DG_WARPS * i);
+            const int i0 = v0 + R::KEYS * (warp + DG_WARPS * i);
+            // Whole stages on one side of the gap between sinks and window: rows at a fixed
+            // distance from the first, addressed by additions.  Others (the gap, the end):
+            // slot by slot.
+            if (i0 + R::KEYS <= v1 && (i0 >= kr.s || i0 + R::KEYS <= kr.s)) {
+                const long long slot0 = kr.slot(i0);
+                const uint8_t *k0 = kb + slot0 * a.ksT + k_lane, *w0 = vb + slot0 * a.vsT + v_lane;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int idx = i0 + 8 * n + g;
-                const uint8_t *row = kb + kr.slot(min(idx, v1 - 1)) * a.ksT;
-                if constexpr (KV4) {
-                    if constexpr (D == 128)
-                        cp16(st + (n * 32 + lane) * 16, row + t * 16, idx < v1);
-                    else
-                        cp_small<8>(st + (n * 32 + lane) * 8, row + t * 8, idx < v1);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c)
-                        cp16(st + ((n * (D / 32) + c) * 32 + lane) * 16, row + c * 64 + t * 16, idx < v1);
+                for (int u = 0; u < R::SUB; ++u) {
+                    copy_k(st + u * R::TILE16, k0, true);
+                    copy_k(st + u * R::TILE16 + R::K_BYTES / 2, k0 + k8, true);
+                    const uint32_t dv = st + u * R::TILE16 + R::K_BYTES;
+                    copy_v(dv, w0, true);
+                    copy_v(dv + R::V_BYTES / 4, w0 + a.vsT, true);
+                    copy_v(dv + R::V_BYTES / 2, w0 + v8, true);
+                    copy_v(dv + 3 * (R::V_BYTES / 4), w0 + v8 + a.vsT, true);
+                    if (u + 1 < R::SUB) {
+                        k0 += 2 * k8;
+                        w0 += 2 * v8;
+                    }
                 }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int idx = i0 + 2 * t + (u & 1) + 8 * (u >> 1);
-                const uint8_t *row = vb + kr.slot(min(idx, v1 - 1)) * a.vsT;
-                if constexpr (KV4) {
-                    cp_small<D / 16>(st + R::K_BYTES + (u * 32 + lane) * (D / 16), row + g * (D / 16), idx < v1);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        cp16(st + R::K_BYTES + ((u * (D / 64) + c) * 32 + lane) * 16, row + c * 128 + g * 16, idx < v1);
+                if constexpr (KV4) {   // lane = key of the stage
+                    cp_small<R::SC_ROW>(st + R::SC_OFF + lane * R::SC_ROW, ksb + slot0 * a.kcT + ks_lane, true);
+                    cp_small<R::SC_ROW>(st + R::SC_OFF + (R::KEYS + lane) * R::SC_ROW, vsb + slot0 * a.vcT + vs_lane, true);
                 }
-            }
-            if constexpr (KV4) {   // lanes 0 .. 15 the keys' scales of K, 16 .. 31 of V
-                const int idx = i0 + (lane & 15);
-                const long long slot = kr.slot(min(idx, v1 - 1));
-                const uint8_t *row = lane < 16 ? ksb + slot * a.kcT : vsb + slot * a.vcT;
-                cp_small<R::SC_ROW>(st + R::K_BYTES + R::V_BYTES + lane * R::SC_ROW, row, idx < v1);
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < R::SUB; ++u) {
+#pragma unroll 1
+                    for (int n = 0; n < 2; ++n) {
+                        const int r = i0 + 16 * u + 8 * n + g;
+                        copy_k(st + u * R::TILE16 + n * (R::K_BYTES / 2), kb + kr.slot(min(r, v1 - 1)) * a.ksT + k_part, r < v1);
+                    }
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = i0 + 16 * u + 2 * t + (x & 1) + 8 * (x >> 1);
+                        copy_v(st + u * R::TILE16 + R::K_BYTES + x * (R::V_BYTES / 4),
+                               vb + kr.slot(min(r, v1 - 1)) * a.vsT + v_part, r < v1);
+                    }
+                }
+                if constexpr (KV4) {
+                    const bool in = i0 + lane < v1;
+                    const long long slot = kr.slot(min(i0 + lane, v1 - 1));
+                    cp_small<R::SC_ROW>(st + R::SC_OFF + lane * R::SC_ROW, ksb + slot * a.kcT, in);
+                    cp_small<R::SC_ROW>(st + R::SC_OFF + (R::KEYS + lane) * R::SC_ROW, vsb + slot * a.vcT, in);
+                }
             }
         }
         cp_commit();   // a group each time, so that the counts below hold
@@ -294,170 +301,229 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
 #pragma unroll
     for (int i = 0; i < R::NS - 1; ++i) issue(i);
 
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // q fragments (B of S^T = K q^T): the d's that lane t contracts, in the order of its K
+    // words, of head g of each group.  4 bits: times a power of two that brings the head's
+    // largest magnitude into [1, 2).  sl2: of the heads 2t, 2t + 1 of each group.
+    uint32_t qb[NH][2 * KS];
+    float sl2[NH][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int x = 0; x < NH; ++x) {
+        const int head = g + 8 * x;
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (long long)b * a.qsB +
+                                  (long long)(hk * a.G + h0 + min(head, nh - 1)) * a.qsH;
+        float mul = a.scale_log2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        for (int c = 0; c < D / 32; ++c) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(qp + (KV4 ? t * (D / 4) + c * 8 : c * 32 + t * 8)));
+            qb[x][4 * c] = u.x;
+            qb[x][4 * c + 1] = u.y;
+            qb[x][4 * c + 2] = u.z;
+            qb[x][4 * c + 3] = u.w;
+        }
+        if constexpr (KV4) {
+            uint32_t big = 0;   // largest magnitude, as bits
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) big = max(big, max(qb[x][i] & 0x7fffu, (qb[x][i] >> 16) & 0x7fffu));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int e = min(max((int)(big >> 7), 1), 253);   // biased exponent
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+            mul *= __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i)
+                qb[x][i] = pack16(__uint_as_float(qb[x][i] << 16) * down, __uint_as_float(qb[x][i] & 0xffff0000u) * down, true);
+        }
+        if (head >= nh) {
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) qb[x][i] = 0u;
+        }
+        sl2[x][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
+        sl2[x][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
+    }
+
+    float o[NH][MT][4], m[NH][2], l[NH][2];
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+        m[x][0] = m[x][1] = -INFINITY;
+        l[x][0] = l[x][1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[x][n][e] = 0.f;
+    }
 
     for (int i = 0; i < mine; ++i) {
-        issue(i + R::NS - 1);     // into the stage of tile i - 1, which every lane has read (__syncwarp below)
-        cp_wait<R::NS - 1>();     // tile i has arrived
+        issue(i + R::NS - 1);     // into the stage of step i - 1, which every lane has read (__syncwarp below)
+        cp_wait<R::NS - 1>();     // stage i has arrived
         __syncwarp();             // for every lane: the scales are shared
         const uint32_t st = ring + (uint32_t)(i % R::NS) * R::STAGE;
-        const int i0 = v0 + 16 * (warp + DG_WARPS * i);
-        float s[2][4];
+        const int i0 = v0 + R::KEYS * (warp + DG_WARPS * i);
+        float s[R::SUB][NH][4];   // [key g, heads 2t, 2t + 1; key g + 8, the same]
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            uint32_t kw[2 * KS];
-            if constexpr (KV4) {
-                uint32_t code[D / 32];
-                const uint32_t sc_at = st + R::K_BYTES + R::V_BYTES + (8 * n + g) * R::SC_ROW;
-                uint32_t sc[2];   // the scale of each 16 codes of the lane, twice in a word
-                if constexpr (D == 128) {
-                    const uint4 u = lds16(st + (n * 32 + lane) * 16);
-                    code[0] = u.x;
-                    code[1] = u.y;
-                    code[2] = u.z;
-                    code[3] = u.w;
-                    const uint32_t p = scales2(lds2b(sc_at + 2 * t));
-                    sc[0] = __byte_perm(p, p, 0x1010);
-                    sc[1] = __byte_perm(p, p, 0x3232);
+        for (int u = 0; u < R::SUB; ++u) {
+            uint32_t kw[2][2 * KS];   // A fragments: the lane's words of the keys g and g + 8
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const uint32_t at = st + u * R::TILE16 + n * (R::K_BYTES / 2);
+                if constexpr (KV4) {
+                    uint32_t code[D / 32], sc[2];   // sc: the scale of each 16 codes of the lane, twice in a word
+                    const uint32_t sc_at = st + R::SC_OFF + (16 * u + 8 * n + g) * R::SC_ROW;
+                    if constexpr (D == 128) {
+                        const uint4 w = lds16(at + lane * 16);
+                        code[0] = w.x;
+                        code[1] = w.y;
+                        code[2] = w.z;
+                        code[3] = w.w;
+                        const uint32_t p = scales2(lds2b(sc_at + 2 * t));
+                        sc[0] = __byte_perm(p, p, 0x1010);
+                        sc[1] = __byte_perm(p, p, 0x3232);
+                    } else {
+                        const uint2 w = lds8(at + lane * 8);
+                        code[0] = w.x;
+                        code[1] = w.y;
+                        const uint32_t p = scales2(lds1b(sc_at + t));
+                        sc[0] = sc[1] = __byte_perm(p, p, 0x1010);
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t f[4];
+                        unpack8(code[c], f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) kw[n][4 * c + e] = hmul2(f[e], sc[c >> 1]);
+                    }
                 } else {
-                    const uint2 u = lds8(st + (n * 32 + lane) * 8);
-                    code[0] = u.x;
-                    code[1] = u.y;
-                    const uint32_t p = scales2(lds1b(sc_at + t));
-                    sc[0] = sc[1] = __byte_perm(p, p, 0x1010);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        const uint4 w = lds16(at + (c * 32 + lane) * 16);
+                        kw[n][4 * c] = w.x;
+                        kw[n][4 * c + 1] = w.y;
+                        kw[n][4 * c + 2] = w.z;
+                        kw[n][4 * c + 3] = w.w;
+                    }
                 }
+            }
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t f[4];
-                    unpack8(code[c], f);
+            for (int x = 0; x < NH; ++x) {
+                s[u][x][0] = s[u][x][1] = s[u][x][2] = s[u][x][3] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) kw[4 * c + e] = hmul2(f[e], sc[c >> 1]);
+                for (int k = 0; k < KS; ++k)
+                    mma16816<KV4>(s[u][x], kw[0][2 * k], kw[1][2 * k], kw[0][2 * k + 1], kw[1][2 * k + 1], qb[x][2 * k],
+                                  qb[x][2 * k + 1]);
+            }
+        }
+        // Scores in log2 units; indices behind the range take no part.  The reference
+        // maximum of a head moves, and O and l with it, only when one of its scores
+        // passes it by more than 2^LAZY: until then p stays below 2^LAZY and no lane has
+        // to know another's scores.
+        const bool inside = i0 + R::KEYS <= v1;
+        bool move = false;
+        float mx[NH][2];
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[x][e] = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < R::SUB; ++u)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float &y = s[u][x][2 * n + e];
+                        y *= sl2[x][e];
+                        if (!inside && i0 + 16 * u + 8 * n + g >= v1) y = -INFINITY;
+                        mx[x][e] = fmaxf(mx[x][e], y);
+                    }
+                move = move || mx[x][e] > m[x][e] + LAZY;
+            }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = mx[x][e];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                    const float m_new = fmaxf(m[x][e], v);
+                    const float alpha = m_new == -INFINITY ? 1.f : ex2(m[x][e] - m_new);
+                    m[x][e] = m_new;
+                    l[x][e] *= alpha;
+#pragma unroll
+                    for (int n = 0; n < MT; ++n) {
+                        o[x][n][e] *= alpha;
+                        o[x][n][2 + e] *= alpha;
+                    }
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < R::SUB; ++u) {
+            uint32_t pb[NH][2];   // B fragments of O^T += V^T P^T: keys 2t, 2t + 1 (+ 8) of head g
+#pragma unroll
+            for (int x = 0; x < NH; ++x) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float base = (m[x][e] == -INFINITY ? 0.f : m[x][e]) - (KV4 ? P_BIAS : 0.f);
+                    p[e] = ex2(s[u][x][e] - base);
+                    p[2 + e] = ex2(s[u][x][2 + e] - base);
+                    l[x][e] += p[e] + p[2 + e];
+                }
+                pb[x][0] = transpose8(pack16(p[0], p[1], KV4));
+                pb[x][1] = transpose8(pack16(p[2], p[3], KV4));
+            }
+            const uint32_t at = st + u * R::TILE16 + R::K_BYTES;
+            if constexpr (KV4) {
+                constexpr int VW = D / 64;   // words of codes per key and lane
+                uint32_t vw[4][VW], vs[2];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (VW == 2) {
+                        const uint2 w = lds8(at + (x * 32 + lane) * 8);
+                        vw[x][0] = w.x;
+                        vw[x][1] = w.y;
+                    } else {
+                        vw[x][0] = lds4b(at + (x * 32 + lane) * 4);
+                    }
+                }
+                const uint32_t sc_at = st + R::SC_OFF + (R::KEYS + 16 * u) * R::SC_ROW + (D == 128 ? g : g >> 1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)   // scales of the keys 2t + 8n, 2t + 1 + 8n
+                    vs[n] = scales2(lds1b(sc_at + (2 * t + 8 * n) * R::SC_ROW) |
+                                    lds1b(sc_at + (2 * t + 1 + 8 * n) * R::SC_ROW) << 8);
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    uint32_t even[2][4], odd[2][4];   // [key half]: (key 2t, key 2t + 1) of the word's even and odd d's
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t p = vw[2 * n][w], q = vw[2 * n + 1][w];
+                        unpack8((p & 0x0f0f0f0fu) | ((q << 4) & 0xf0f0f0f0u), even[n]);
+                        unpack8(((p >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u), odd[n]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a0 = hmul2(even[0][e], vs[0]), a1 = hmul2(odd[0][e], vs[0]);
+                        const uint32_t a2 = hmul2(even[1][e], vs[1]), a3 = hmul2(odd[1][e], vs[1]);
+#pragma unroll
+                        for (int x = 0; x < NH; ++x) mma16816<true>(o[x][4 * w + e], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+                    }
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    const uint4 u = lds16(st + ((n * (D / 32) + c) * 32 + lane) * 16);
-                    kw[4 * c] = u.x;
-                    kw[4 * c + 1] = u.y;
-                    kw[4 * c + 2] = u.z;
-                    kw[4 * c + 3] = u.w;
-                }
-            }
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t vw[4][4];
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-                mma16816<KV4>(s[n], qa[k][0], HALVES == 2 ? qa[k][2 * HALVES - 2] : 0u, qa[k][1],
-                              HALVES == 2 ? qa[k][2 * HALVES - 1] : 0u, kw[2 * k], kw[2 * k + 1]);
-        }
-        // scores in log2 units; indices behind the range take no part
-        float mx[2] = {-INFINITY, -INFINITY};
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 w = lds16(at + ((x * (D / 64) + c) * 32 + lane) * 16);
+                        vw[x][0] = w.x;
+                        vw[x][1] = w.y;
+                        vw[x][2] = w.z;
+                        vw[x][3] = w.w;
+                    }
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a0 = __byte_perm(vw[0][e], vw[1][e], 0x5410), a1 = __byte_perm(vw[0][e], vw[1][e], 0x7632);
+                        const uint32_t a2 = __byte_perm(vw[2][e], vw[3][e], 0x5410), a3 = __byte_perm(vw[2][e], vw[3][e], 0x7632);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool in = i0 + 8 * n + 2 * t + e < v1;
-#pragma unroll
-                for (int hf = 0; hf < HALVES; ++hf) {
-                    float &x = s[n][2 * hf + e];
-                    x = in ? x * sl2[hf] : -INFINITY;
-                    mx[hf] = fmaxf(mx[hf], x);
-                }
-            }
-        bool move = false;
-#pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf) {
-            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
-            move = move || mx[hf] > m[hf] + LAZY;
-        }
-        // The reference maximum moves, and O and l with it, only when a row's maximum
-        // passes it by more than 2^LAZY; p stays below 2^LAZY until then.
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf) {
-                const float m_new = fmaxf(m[hf], mx[hf]);
-                const float alpha = m_new == -INFINITY ? 1.f : ex2(m[hf] - m_new);
-                m[hf] = m_new;
-                l[hf] *= alpha;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[n][2 * hf] *= alpha;
-                    o[n][2 * hf + 1] *= alpha;
-                }
-            }
-        }
-        uint32_t pa[2][2];   // [key half][row half]
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            if (hf >= HALVES) {
-                pa[0][hf] = pa[1][hf] = 0u;
-                continue;
-            }
-            const float base = (m[hf] == -INFINITY ? 0.f : m[hf]) - (KV4 ? P_BIAS : 0.f);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = ex2(s[n][2 * hf] - base), p1 = ex2(s[n][2 * hf + 1] - base);
-                l[hf] += p0 + p1;
-                pa[n][hf] = pack16(p0, p1, KV4);
-            }
-        }
-        if constexpr (KV4) {
-            constexpr int VW = D / 64;   // words of codes per key and lane
-            uint32_t vw[4][VW], vs[2];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t at = st + R::K_BYTES + (u * 32 + lane) * (D / 16);
-                if constexpr (VW == 2) {
-                    const uint2 x = lds8(at);
-                    vw[u][0] = x.x;
-                    vw[u][1] = x.y;
-                } else {
-                    vw[u][0] = lds4b(at);
-                }
-            }
-            const uint32_t sc_at = st + R::K_BYTES + R::V_BYTES + 16 * R::SC_ROW + (D == 128 ? g : g >> 1);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)   // scales of the keys 2t + 8u, 2t + 1 + 8u
-                vs[u] = scales2(lds1b(sc_at + (2 * t + 8 * u) * R::SC_ROW) | lds1b(sc_at + (2 * t + 1 + 8 * u) * R::SC_ROW) << 8);
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                uint32_t even[2][4], odd[2][4];   // [key half]: (key 2t, key 2t + 1) of the word's even and odd d's
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t x = vw[2 * u][w], y = vw[2 * u + 1][w];
-                    unpack8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), even[u]);
-                    unpack8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd[u]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mma16816<true>(o[8 * w + 2 * e], pa[0][0], pa[0][1], pa[1][0], pa[1][1], hmul2(even[0][e], vs[0]),
-                                   hmul2(even[1][e], vs[1]));
-                    mma16816<true>(o[8 * w + 2 * e + 1], pa[0][0], pa[0][1], pa[1][0], pa[1][1], hmul2(odd[0][e], vs[0]),
-                                   hmul2(odd[1][e], vs[1]));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t vw[4][4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint4 x = lds16(st + R::K_BYTES + ((u * (D / 64) + c) * 32 + lane) * 16);
-                    vw[u][0] = x.x;
-                    vw[u][1] = x.y;
-                    vw[u][2] = x.z;
-                    vw[u][3] = x.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-                    mma16816<false>(o[8 * c + e], pa[0][0], pa[0][1], pa[1][0], pa[1][1],
-                                    __byte_perm(vw[0][e >> 1], vw[1][e >> 1], sel),
-                                    __byte_perm(vw[2][e >> 1], vw[3][e >> 1], sel));
+                        for (int x = 0; x < NH; ++x) mma16816<false>(o[x][4 * c + e], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+                    }
                 }
             }
         }
@@ -467,31 +533,31 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
     cp_wait<0>();
     __syncthreads();   // every warp is done with its ring: the merge area overlays it
 
-    // Join the warps: row r's (m, l) and O of each warp, then one weighted sum.
-    float *mo = reinterpret_cast<float *>(dg_smem);                    // [warp][16][D]
-    float *mm = mo + DG_WARPS * 8 * HALVES * D, *ml = mm + DG_WARPS * 16;   // [warp][16]
+    // Join the warps: each head's (m, l) and O of each warp, then one weighted sum.
+    float *mo = reinterpret_cast<float *>(dg_smem);                     // [warp][8 NH][D]
+    float *mm = mo + DG_WARPS * 8 * NH * D, *ml = mm + DG_WARPS * 16;   // [warp][16]
 #pragma unroll
-    for (int hf = 0; hf < HALVES; ++hf) {
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-        l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-        const int row = g + 8 * hf;
-        if (t == 0) {
-            mm[warp * 16 + row] = m[hf];
-            ml[warp * 16 + row] = l[hf];
-        }
+    for (int x = 0; x < NH; ++x)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+            const int row = 8 * x + 2 * t + e;
+            float sum = l[x][e];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // column 2t + e of tile n belongs to the d's of lane group 2t + e
-                const int gg = 2 * t + e;
-                const int d = KV4 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
-                mo[(warp * 8 * HALVES + row) * D + d] = o[n][2 * hf + e];
+            for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (g == 0) {
+                mm[warp * 16 + row] = m[x][e];
+                ml[warp * 16 + row] = sum;
             }
-    }
+            float *dst = mo + (warp * 8 * NH + row) * D;
+#pragma unroll
+            for (int n = 0; n < MT; ++n) {   // rows g and g + 8 of tile n: an even d of lane group g and the next one
+                const int d = KV4 ? g * (D / 8) + 2 * n : (n >> 2) * 64 + g * 8 + 2 * (n & 3);
+                *reinterpret_cast<float2 *>(dst + d) = make_float2(o[x][n][e], o[x][n][2 + e]);
+            }
+        }
     __syncthreads();
-    for (int x = threadIdx.x; x < nh * D; x += DG_WARPS * 32) {
-        const int row = x / D, d = x % D;
+    for (int y = threadIdx.x; y < nh * D; y += DG_WARPS * 32) {
+        const int row = y / D, d = y % D;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < DG_WARPS; ++w) M = fmaxf(M, mm[w * 16 + row]);
@@ -501,7 +567,7 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
             for (int w = 0; w < DG_WARPS; ++w) {
                 const float wt = ex2(mm[w * 16 + row] - M);
                 L += wt * ml[w * 16 + row];
-                acc += wt * mo[(w * 8 * HALVES + row) * D + d];
+                acc += wt * mo[(w * 8 * NH + row) * D + d];
             }
         }
         store_split(a, b, hk * a.G + h0 + row, split, d, M - (KV4 ? P_BIAS : 0.f), L, acc);
@@ -683,10 +749,10 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeGroupArgs 
     }
 }
 
-template <int D, bool KV4, int HALVES>
+template <int D, bool KV4, int NH>
 int launch_mma(const DecodeGroupArgs &a, cudaStream_t s) {
-    auto kern = decode_mma_kernel<D, KV4, HALVES>;
-    constexpr int merge = DG_WARPS * (8 * HALVES * D + 32) * 4;
+    auto kern = decode_mma_kernel<D, KV4, NH>;
+    constexpr int merge = DG_WARPS * (8 * NH * D + 32) * 4;
     constexpr int smem = Ring<D, KV4>::BYTES > merge ? Ring<D, KV4>::BYTES : merge;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BA_ERR_CUDA;
     kern<<<dim3(a.n_splits, a.B * a.Hkv, (a.G + 15) / 16), DG_WARPS * 32, smem, s>>>(a);
