@@ -9,6 +9,7 @@ loaded they raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -173,7 +174,7 @@ def load(path: str | None = None):
     lib.attn_decode_fwd.restype = i
     lib.attn_decode_fwd.argtypes = [T, T, T, i, i, i, i, i, vp, i, f, vp, i, vp, vp, sz, vp]
     lib.attn_window_fwd_workspace_size.restype = sz
-    lib.attn_window_fwd_workspace_size.argtypes = []
+    lib.attn_window_fwd_workspace_size.argtypes = [i, i, i, i, i]
     lib.attn_window_fwd.restype = i
     lib.attn_window_fwd.argtypes = [T, T, T, i, i, i, i, i, i, i, i64, i, i, vp, i64, f, vp, i, vp, vp, sz, vp]
     lib.attn_window_bwd_workspace_size.restype = sz
@@ -501,60 +502,101 @@ def ulysses_attn_fwd(q_tok, k_tok, v_tok, *, key_padding_mask=None, attn_mask=No
     return out, lse
 
 
-def _like(ref, **tensors):
-    """Every tensor on ref's device, and that device the current one (launches and torch's streams go there)."""
-    if ref.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {ref.device}, but the current device is cuda:{torch.cuda.current_device()}")
+# Helpers of the entry points below.  A single-token call is over on the GPU in a few
+# microseconds, so what the binding does per call is kept short: one stride() per tensor,
+# devices and streams as integers, sizes of workspaces remembered.
+
+_DTYPES = {torch.float32: BA_F32, torch.bfloat16: BA_BF16}
+
+
+def _code(dtype):
+    c = _DTYPES.get(dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return c
+
+
+def _view(name, x):
+    """(pointer, strides) of a (B, H, T, d) tensor."""
+    s = x.stride()
+    if len(s) != 4 or s[3] != 1 and x.shape[3] > 1:
+        raise ValueError(f"{name}: expected a (B, H, T, d) tensor with a contiguous last axis")
+    return ba_tensor(x.data_ptr(), s[0], s[1], s[2])
+
+
+def _device(ref, **tensors):
+    """Index of ref's device: the current one (launches and torch's streams go there), and every tensor's."""
+    dev = ref.get_device()
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
     for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return dev
+
+
+def _on_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _kv_heads(q, k, v):
-    """Checks k, v (B, Hkv, L, d) against q (B, Hq, .., d) and returns (Hkv, L)."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+    """Checks k, v (B, Hkv, L, d) against q (B, Hq, .., d) and returns (B, Hq, Lq, d, Hkv, L)."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or ks != v.shape:
         raise ValueError("expected q (B, Hq, L, d) and k, v (B, Hkv, L, d) of one shape")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k and v must share a dtype")
-    if k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
-        raise ValueError(f"k, v of shape {tuple(k.shape)} do not match q of shape {tuple(q.shape)}")
-    Hkv = k.shape[1]
-    if Hkv == 0 or q.shape[1] % Hkv:
-        raise ValueError(f"{q.shape[1]} query heads are not a multiple of {Hkv} key heads")
-    return Hkv, k.shape[2]
+    B, Hq, Lq, d = qs
+    Bk, Hkv, Lk, dk = ks
+    if Bk != B or dk != d:
+        raise ValueError(f"k, v of shape {tuple(ks)} do not match q of shape {tuple(qs)}")
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
+    return B, Hq, Lq, d, Hkv, Lk
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor from the memory of the stream that the call runs on (so that nothing
-    still pending on another stream uses the memory, and its reuse waits for this call)."""
+def _empty(ref, shape, dtype, stream):
+    """A new tensor beside ref, from the memory of the stream that the call runs on (so that
+    nothing still pending on another stream uses the memory, and its reuse waits for this call)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return ref.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return ref.new_empty(shape, dtype=dtype)
+
+
+def _buffer(ref, name, t, shape, dtype, stream):
+    """An output: t checked (contiguous, of the shape and dtype, on ref's device), or a new one."""
+    if t is None:
+        return _empty(ref, shape, dtype, stream)
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != ref.get_device():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {ref.device}")
+    return t
 
 
 def _out_pair(q, out, out_dtype, lse, stream):
-    """The outputs of an attention call on q: allocated, or the caller's checked."""
-    if out is None:
-        out = _empty(q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out does not have out_dtype")
-    if lse is None:
-        lse = _empty(q.shape[:3], torch.float32, q.device, stream)
-    _check_out(out, lse, q.shape)
-    _like(q, out=out, lse=lse)
-    return out, lse
+    """out and lse of an attention call on q."""
+    if out_dtype is None:
+        out_dtype = q.dtype if out is None else out.dtype
+    return _buffer(q, "out", out, q.shape, out_dtype, stream), _buffer(q, "lse", lse, q.shape[:3], torch.float32, stream)
 
 
-def _scratch(need, workspace, device, stream):
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn, dev, *sizes):
+    """Bytes that a *_workspace_size query gives for these sizes on device dev (the current one)."""
+    return getattr(load(), fn)(*sizes)
+
+
+def _scratch(ref, need, workspace, stream):
     """(pointer, bytes, tensor) of a workspace: the caller's or a new one (the tensor is kept until the launch)."""
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _empty((need,), torch.uint8, device, stream)
-    elif not workspace.is_contiguous() or workspace.dtype != torch.uint8 or workspace.device != device:
+        workspace = _empty(ref, (need,), torch.uint8, stream)
+    elif not workspace.is_contiguous() or workspace.dtype != torch.uint8 or workspace.get_device() != ref.get_device():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def _c_int(name, x, lo):
@@ -570,17 +612,17 @@ def attn_window_fwd(q, k, v, *, window, sinks=0, q_off=0, key_padding_mask=None,
     q (B, Hq, Lq, d) at positions q_off + i against k, v (B, Hkv, Lk, d) at positions
     0 .. Lk - 1, Hkv dividing Hq; see include/blockattn.h.  Returns (out, lse)."""
     lib = load()
-    Hkv, Lk = _kv_heads(q, k, v)
-    B, Hq, Lq, d = q.shape
+    B, Hq, Lq, d, Hkv, Lk = _kv_heads(q, k, v)
     window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
-    tq, tk, tv = _tensor(q), _tensor(k), _tensor(v)
-    _like(q, k=k, v=v, key_padding_mask=key_padding_mask)
+    dt = _code(q.dtype)
+    dev = _device(q, k=k, v=v, key_padding_mask=key_padding_mask)
     out, lse = _out_pair(q, out, out_dtype, lse, stream)
     kpm, kpm_ld = _mask(key_padding_mask, B, Lk, "key_padding_mask")
-    ws, ws_bytes, keep = _scratch(lib.attn_window_fwd_workspace_size(), workspace, q.device, stream)
-    rc = lib.attn_window_fwd(tq, tk, tv, B, Hq, Hkv, Lq, Lk, d, _dtype_code(q.dtype), q_off, window, sinks, kpm, kpm_ld,
-                             0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
-                             ws, ws_bytes, _stream(stream))
+    need = _workspace_bytes("attn_window_fwd_workspace_size", dev, B, Hq, Lq, d, dt)
+    ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
+    rc = lib.attn_window_fwd(_view("q", q), _view("k", k), _view("v", v), B, Hq, Hkv, Lq, Lk, d, dt, q_off, window, sinks,
+                             kpm, kpm_ld, 0.0 if scale is None else float(scale), out.data_ptr(), _code(out.dtype),
+                             lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_window_fwd", rc)
     return out, lse
 
@@ -590,28 +632,23 @@ def attn_window_bwd(q, k, v, out, dout, lse, *, window, sinks=0, q_off=0, key_pa
     """Gradients (dq, dk, dv) of attn_window_fwd from its out and lse; of q's dtype
     unless grad_dtype (or the given buffers) say float32; see include/blockattn.h."""
     lib = load()
-    Hkv, Lk = _kv_heads(q, k, v)
-    B, Hq, Lq, d = q.shape
+    B, Hq, Lq, d, Hkv, Lk = _kv_heads(q, k, v)
     window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
-    tensors = _tensor(q), _tensor(k), _tensor(v), _tensor(out), _tensor(dout)
+    dt = _code(q.dtype)
     _check_bwd_inputs(q, out, dout, lse)
-    _like(q, k=k, v=v, out=out, dout=dout, lse=lse, key_padding_mask=key_padding_mask, dq=dq, dk=dk, dv=dv)
-    given = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype)
-    grad_dtype = given if grad_dtype is None else grad_dtype
-    grads = []
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if t is None:
-            t = _empty(like.shape, grad_dtype, q.device, stream)
-        elif t.dtype != grad_dtype or not t.is_contiguous() or t.shape != like.shape:
-            raise ValueError(f"{name} must be a contiguous {grad_dtype} CUDA tensor of shape {tuple(like.shape)}")
-        grads.append(t)
-    dq, dk, dv = grads
+    dev = _device(q, k=k, v=v, out=out, dout=dout, lse=lse, key_padding_mask=key_padding_mask)
+    if grad_dtype is None:
+        grad_dtype = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype)
+    dq = _buffer(q, "dq", dq, q.shape, grad_dtype, stream)
+    dk = _buffer(q, "dk", dk, k.shape, grad_dtype, stream)
+    dv = _buffer(q, "dv", dv, v.shape, grad_dtype, stream)
     kpm, kpm_ld = _mask(key_padding_mask, B, Lk, "key_padding_mask")
-    need = lib.attn_window_bwd_workspace_size(B, Hq, Hkv, Lq, Lk, d, q_off, window, sinks)
-    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
-    rc = lib.attn_window_bwd(*tensors, _ptr(lse), B, Hq, Hkv, Lq, Lk, d, _dtype_code(q.dtype), q_off, window, sinks,
-                             kpm, kpm_ld, 0.0 if scale is None else float(scale), _ptr(dq), _ptr(dk), _ptr(dv),
-                             _dtype_code(grad_dtype), ws, ws_bytes, _stream(stream))
+    need = _workspace_bytes("attn_window_bwd_workspace_size", dev, B, Hq, Hkv, Lq, Lk, d, q_off, window, sinks)
+    ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
+    rc = lib.attn_window_bwd(_view("q", q), _view("k", k), _view("v", v), _view("out", out), _view("dout", dout),
+                             lse.data_ptr(), B, Hq, Hkv, Lq, Lk, d, dt, q_off, window, sinks, kpm, kpm_ld,
+                             0.0 if scale is None else float(scale), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                             _code(grad_dtype), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_window_bwd", rc)
     return dq, dk, dv
 
@@ -646,13 +683,13 @@ def attn_decode_fwd(q, k_cache, v_cache, *, lengths=None, num_splits=0, scale=No
     return out, lse
 
 
-def _per_sequence(name, t, B, ref):
+def _per_sequence(name, t, B, dev):
+    """Pointer of an int32 entry for each sequence, or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_cuda or t.numel() != B or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {B} entries")
-    _like(ref, **{name: t})
-    return ctypes.c_void_p(t.data_ptr())
+    if t.dtype != torch.int32 or t.get_device() != dev or t.numel() != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {B} entries on cuda:{dev}")
+    return t.data_ptr()
 
 
 def attn_window_decode_fwd(q, k_cache, v_cache, *, window, sinks=0, lengths=None, scale=None, out=None, out_dtype=None,
@@ -661,20 +698,19 @@ def attn_window_decode_fwd(q, k_cache, v_cache, *, window, sinks=0, lengths=None
     against the caches (B, Hkv, S, d), Hkv dividing Hq; lengths: int32 (B) or None (S).
     Returns (out, lse)."""
     lib = load()
-    Hkv, S = _kv_heads(q, k_cache, v_cache)
-    B, Hq, one, d = q.shape
+    B, Hq, one, d, Hkv, S = _kv_heads(q, k_cache, v_cache)
     if one != 1:
         raise ValueError("decode takes one query per (b, h): q of shape (B, Hq, 1, d)")
     window, sinks = _c_int("window", window, 1), _c_int("sinks", sinks, 0)
-    tq, tk, tv = _tensor(q), _tensor(k_cache), _tensor(v_cache)
-    _like(q, k_cache=k_cache, v_cache=v_cache)
-    lens = _per_sequence("lengths", lengths, B, q)
+    dt = _code(q.dtype)
+    dev = _device(q, k_cache=k_cache, v_cache=v_cache)
+    lens = _per_sequence("lengths", lengths, B, dev)
     out, lse = _out_pair(q, out, out_dtype, lse, stream)
-    need = lib.attn_window_decode_workspace_size(B, Hq, Hkv, S, d, window, sinks)
-    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
-    rc = lib.attn_window_decode_fwd(tq, tk, tv, B, Hq, Hkv, S, d, _dtype_code(q.dtype), lens, window, sinks,
-                                    0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
-                                    ws, ws_bytes, _stream(stream))
+    need = _workspace_bytes("attn_window_decode_workspace_size", dev, B, Hq, Hkv, S, d, window, sinks)
+    ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
+    rc = lib.attn_window_decode_fwd(_view("q", q), _view("k_cache", k_cache), _view("v_cache", v_cache), B, Hq, Hkv, S, d,
+                                    dt, lens, window, sinks, 0.0 if scale is None else float(scale), out.data_ptr(),
+                                    _code(out.dtype), lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_window_decode_fwd", rc)
     return out, lse
 
@@ -718,12 +754,13 @@ def kv4_append(cache, k, v, *, start=None, counts=None, stream=None):
     start, counts: int32 (B) CUDA tensors or None (0, T).  Slots outside the cache are dropped."""
     lib = load()
     B, H, S, d = cache.shape
-    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[:2] != (B, H) or k.shape[3] != d:
-        raise ValueError(f"k, v of shape {tuple(k.shape)} do not match a cache of {cache.shape}")
-    tk, tv = _tensor(k), _tensor(v)
-    _like(k, v=v, cache=cache.k_codes)
-    rc = lib.kv4_append(tk, tv, cache._c, B, H, k.shape[2], S, d, _dtype_code(k.dtype), _per_sequence("start", start, B, k),
-                        _per_sequence("counts", counts, B, k), _stream(stream))
+    shape = k.shape
+    if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype or shape[0] != B or shape[1] != H or shape[3] != d:
+        raise ValueError(f"k, v of shape {tuple(shape)} do not match a cache of {cache.shape}")
+    dev = _device(k, v=v, cache=cache.k_codes)
+    rc = lib.kv4_append(_view("k", k), _view("v", v), cache._c, B, H, shape[2], S, d, _code(k.dtype),
+                        _per_sequence("start", start, B, dev), _per_sequence("counts", counts, B, dev),
+                        _on_stream(stream, dev))
     _check("kv4_append", rc)
     return cache
 
@@ -732,18 +769,14 @@ def kv4_read(cache, T, *, first=0, dtype=torch.bfloat16, out_k=None, out_v=None,
     """The values of slots first .. first + T - 1 of a KV4Cache: (k, v), each (B, H, T, d)."""
     lib = load()
     B, H, S, d = cache.shape
-    T, first = _c_int("T", T, 0), _c_int("first", first, 0)
-    outs = []
-    for name, t in (("out_k", out_k), ("out_v", out_v)):
-        if t is None:
-            t = _empty((B, H, T, d), dtype, cache.k_codes.device, stream)
-        elif tuple(t.shape) != (B, H, T, d) or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(B, H, T, d)}")
-        outs.append(t)
-    _like(cache.k_codes, out_k=outs[0], out_v=outs[1])
-    rc = lib.kv4_read(cache._c, B, H, S, d, first, T, _dtype_code(dtype), _ptr(outs[0]), _ptr(outs[1]), _stream(stream))
+    T, first, dt = _c_int("T", T, 0), _c_int("first", first, 0), _code(dtype)
+    codes = cache.k_codes
+    dev = _device(codes)
+    k = _buffer(codes, "out_k", out_k, (B, H, T, d), dtype, stream)
+    v = _buffer(codes, "out_v", out_v, (B, H, T, d), dtype, stream)
+    rc = lib.kv4_read(cache._c, B, H, S, d, first, T, dt, k.data_ptr(), v.data_ptr(), _on_stream(stream, dev))
     _check("kv4_read", rc)
-    return outs[0], outs[1]
+    return k, v
 
 
 def attn_decode_kv4_fwd(q, cache, *, lengths=None, window=0, sinks=0, scale=None, out=None, out_dtype=None, lse=None,
@@ -752,19 +785,19 @@ def attn_decode_kv4_fwd(q, cache, *, lengths=None, window=0, sinks=0, scale=None
     every key (window = 0) or a window with sinks; see include/blockattn.h.  Returns (out, lse)."""
     lib = load()
     B, Hkv, S, d = cache.shape
-    if q.dim() != 4 or q.shape[0] != B or q.shape[2] != 1 or q.shape[3] != d or Hkv == 0 or q.shape[1] % Hkv:
-        raise ValueError(f"q of shape {tuple(q.shape)} does not match a cache of {cache.shape}")
-    Hq = q.shape[1]
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != 1 or shape[3] != d or Hkv == 0 or shape[1] % Hkv:
+        raise ValueError(f"q of shape {tuple(shape)} does not match a cache of {cache.shape}")
+    Hq = shape[1]
     window, sinks = _c_int("window", window, 0), _c_int("sinks", sinks, 0)
-    tq = _tensor(q)
-    _like(q, cache=cache.k_codes)
-    lens = _per_sequence("lengths", lengths, B, q)
+    dev = _device(q, cache=cache.k_codes)
+    lens = _per_sequence("lengths", lengths, B, dev)
     out, lse = _out_pair(q, out, out_dtype, lse, stream)
-    need = lib.attn_decode_kv4_workspace_size(B, Hq, Hkv, S, d, window, sinks)
-    ws, ws_bytes, keep = _scratch(need, workspace, q.device, stream)
-    rc = lib.attn_decode_kv4_fwd(tq, cache._c, B, Hq, Hkv, S, d, _dtype_code(q.dtype), lens, window, sinks,
-                                 0.0 if scale is None else float(scale), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
-                                 ws, ws_bytes, _stream(stream))
+    need = _workspace_bytes("attn_decode_kv4_workspace_size", dev, B, Hq, Hkv, S, d, window, sinks)
+    ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
+    rc = lib.attn_decode_kv4_fwd(_view("q", q), cache._c, B, Hq, Hkv, S, d, _code(q.dtype), lens, window, sinks,
+                                 0.0 if scale is None else float(scale), out.data_ptr(), _code(out.dtype),
+                                 lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_decode_kv4_fwd", rc)
     return out, lse
 
@@ -793,25 +826,24 @@ def rope_apply(x, *, x2=None, base=10000.0, positions=None, pos_scale=1.0, out=N
 def _norm_inputs(q, k, wq, wk, positions):
     """Checks of qk_norm_rope_*: ((B, Hq, Hkv, T, d), weight dtype code, positions pointer, ld)."""
     B, Hq, T, d = q.shape
-    if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
+    Bk, Hkv, Tk, dk = k.shape
+    if Bk != B or Tk != T or dk != d:
         raise ValueError(f"k of shape {tuple(k.shape)} does not match q of shape {tuple(q.shape)}")
-    if k.dtype != q.dtype or wq.dtype != wk.dtype or wq.dtype not in (q.dtype, torch.float32):
+    if k.dtype != q.dtype or wq.dtype != wk.dtype or (wq.dtype != q.dtype and wq.dtype != torch.float32):
         raise TypeError("q and k share a dtype; the weights have it too or are float32")
-    for name, w in (("wq", wq), ("wk", wk)):
-        if tuple(w.shape) != (d,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of {d} entries")
-    _like(q, k=k, wq=wq, wk=wk, positions=positions)
-    ld = 0
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T or \
-                (T > 1 and positions.stride(-1) != 1) or (positions.dim() == 2 and positions.shape[0] not in (1, B)):
-            raise ValueError(f"positions must be an int32 CUDA tensor (T,) or (B, T) with T = {T}")
-        if positions.dim() == 2 and positions.shape[0] == B and B > 1:
-            ld = positions.stride(0)
-            if ld < T:   # (an expanded row is shared by all)
-                if ld != 0:
-                    raise ValueError("the rows of positions overlap")
-    return (B, Hq, k.shape[1], T, d), _dtype_code(wq.dtype), _ptr(positions), ld
+    if wq.shape != (d,) or wk.shape != (d,) or not wq.is_contiguous() or not wk.is_contiguous():
+        raise ValueError(f"wq and wk must be contiguous tensors of {d} entries")
+    if positions is None:
+        return (B, Hq, Hkv, T, d), _code(wq.dtype), None, 0
+    shape, s, ld = positions.shape, positions.stride(), 0
+    if positions.dtype != torch.int32 or len(shape) not in (1, 2) or shape[-1] != T or (T > 1 and s[-1] != 1) or \
+            (len(shape) == 2 and shape[0] not in (1, B)):
+        raise ValueError(f"positions must be an int32 CUDA tensor (T,) or (B, T) with T = {T}")
+    if len(shape) == 2 and shape[0] == B and B > 1 and s[0] != 0:   # (an expanded row is shared by all)
+        ld = s[0]
+        if ld < T:
+            raise ValueError("the rows of positions overlap")
+    return (B, Hq, Hkv, T, d), _code(wq.dtype), positions.data_ptr(), ld
 
 
 def qk_norm_rope_fwd(q, k, wq, wk, *, eps=1e-6, positions=None, base=10000.0, pos_scale=1.0, out_q=None, out_k=None,
@@ -820,20 +852,14 @@ def qk_norm_rope_fwd(q, k, wq, wk, *, eps=1e-6, positions=None, base=10000.0, po
     wq, wk (d); positions: int32 (T,) or (B, T), None: 0 .. T - 1; see include/blockattn.h.
     Returns (yq, yk), contiguous."""
     lib = load()
-    tq, tk = _tensor(q), _tensor(k)
+    tq, tk = _view("q", q), _view("k", k)
     sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
-    outs = []
-    for name, y, x in (("out_q", out_q, q), ("out_k", out_k, k)):
-        if y is None:
-            y = _empty(x.shape, q.dtype, q.device, stream)
-        elif y.shape != x.shape or y.dtype != q.dtype or not y.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor of shape {tuple(x.shape)}")
-        outs.append(y)
-    _like(q, out_q=outs[0], out_k=outs[1])
-    rc = lib.qk_norm_rope_fwd(tq, tk, _ptr(wq), _ptr(wk), wdt, *sizes, _dtype_code(q.dtype), float(eps), pos, ld,
-                              float(base), float(pos_scale), _ptr(outs[0]), _ptr(outs[1]), _stream(stream))
+    dev = _device(q, k=k, wq=wq, wk=wk, positions=positions)
+    yq, yk = _buffer(q, "out_q", out_q, q.shape, q.dtype, stream), _buffer(q, "out_k", out_k, k.shape, q.dtype, stream)
+    rc = lib.qk_norm_rope_fwd(tq, tk, wq.data_ptr(), wk.data_ptr(), wdt, *sizes, _code(q.dtype), float(eps), pos, ld,
+                              float(base), float(pos_scale), yq.data_ptr(), yk.data_ptr(), _on_stream(stream, dev))
     _check("qk_norm_rope_fwd", rc)
-    return outs[0], outs[1]
+    return yq, yk
 
 
 def qk_norm_rope_bwd(q, k, wq, wk, dyq, dyk, *, eps=1e-6, positions=None, base=10000.0, pos_scale=1.0, dq=None, dk=None,
@@ -841,29 +867,23 @@ def qk_norm_rope_bwd(q, k, wq, wk, dyq, dyk, *, eps=1e-6, positions=None, base=1
     """Gradients (dq, dk, dwq, dwk) of qk_norm_rope_fwd for dyq, dyk (of q's dtype or
     float32): dq, dk of q's dtype, dwq, dwk float32."""
     lib = load()
-    tq, tk, tgq, tgk = _tensor(q), _tensor(k), _tensor(dyq), _tensor(dyk)
+    tensors = _view("q", q), _view("k", k), _view("dyq", dyq), _view("dyk", dyk)
     sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
     if dyq.shape != q.shape or dyk.shape != k.shape:
         raise ValueError("dyq and dyk must have the shapes of q and k")
-    if dyq.dtype != dyk.dtype or dyq.dtype not in (q.dtype, torch.float32):
+    if dyq.dtype != dyk.dtype or (dyq.dtype != q.dtype and dyq.dtype != torch.float32):
         raise TypeError("dyq and dyk have the dtype of q or are float32")
-    grads = []
-    for name, t, x in (("dq", dq, q), ("dk", dk, k)):
-        if t is None:
-            t = _empty(x.shape, q.dtype, q.device, stream)
-        elif t.shape != x.shape or t.dtype != q.dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor of shape {tuple(x.shape)}")
-        grads.append(t)
-    _like(q, dyq=dyq, dyk=dyk, dq=grads[0], dk=grads[1])
-    d = sizes[4]
-    dw = _empty((2, d), torch.float32, q.device, stream)
-    ws, ws_bytes, keep = _scratch(lib.qk_norm_rope_bwd_workspace_size(*sizes, _dtype_code(q.dtype)), workspace, q.device,
-                                  stream)
-    rc = lib.qk_norm_rope_bwd(tq, tk, _ptr(wq), _ptr(wk), wdt, tgq, tgk, _dtype_code(dyq.dtype), *sizes,
-                              _dtype_code(q.dtype), float(eps), pos, ld, float(base), float(pos_scale), _ptr(grads[0]),
-                              _ptr(grads[1]), _ptr(dw[0]), _ptr(dw[1]), ws, ws_bytes, _stream(stream))
+    dev = _device(q, k=k, wq=wq, wk=wk, positions=positions, dyq=dyq, dyk=dyk)
+    dt, d = _code(q.dtype), sizes[4]
+    dq, dk = _buffer(q, "dq", dq, q.shape, q.dtype, stream), _buffer(q, "dk", dk, k.shape, q.dtype, stream)
+    dwq, dwk = _empty(q, (2, d), torch.float32, stream).unbind(0)
+    ws, ws_bytes, keep = _scratch(q, _workspace_bytes("qk_norm_rope_bwd_workspace_size", dev, *sizes, dt), workspace, stream)
+    rc = lib.qk_norm_rope_bwd(tensors[0], tensors[1], wq.data_ptr(), wk.data_ptr(), wdt, tensors[2], tensors[3],
+                              _code(dyq.dtype), *sizes, dt, float(eps), pos, ld, float(base), float(pos_scale),
+                              dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), ws, ws_bytes,
+                              _on_stream(stream, dev))
     _check("qk_norm_rope_bwd", rc)
-    return grads[0], grads[1], dw[0], dw[1]
+    return dq, dk, dwq, dwk
 
 
 def tile_classes(B, Lq, Lk, *, q_off=0, k_off=0, key_padding_mask=None, attn_mask=None, causal=False,

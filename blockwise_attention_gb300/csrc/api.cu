@@ -1840,7 +1840,13 @@ int window_heads_per_group(int B, int Hq, int Hkv, long long keys, int d, int dt
 
 }  // namespace
 
-size_t attn_window_fwd_workspace_size(void) { return sched_bytes(1); }
+// The item counter, for launches of more items than SMs.
+size_t attn_window_fwd_workspace_size(int B, int Hq, int Lq, int d, int dtype) {
+    if (B < 1 || Hq < 1 || Lq < 1 || !tc_supported(dtype, d)) return 0;
+    const int dev = current_device();
+    const int sms = dev >= 0 && g_num_sms[dev] > 0 ? g_num_sms[dev] : 0;
+    return (long long)ceil_div(Lq, 2 * TILE) * B * Hq > sms ? sched_bytes(1) : 0;
+}
 
 int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hkv, int Lq, int Lk, int d, int dtype,
                     int64_t q_off, int window, int sinks, const uint8_t *key_padding_mask, int64_t kpm_ld, float scale,
@@ -2094,27 +2100,36 @@ int attn_decode_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int H, int S, 
 
 namespace {
 
-// Most keys that a sequence can see, and the splits of that range.
+// Most keys that a sequence can see.
 long long most_keys(int S, int window, int sinks) {
     if (window == 0) return S;
     const long long n = (long long)window + sinks;
     return n < S ? n : S;
 }
 
-size_t decode_group_bytes(long long rows, int n_splits, int d) {
-    if (n_splits <= 1) return 0;
-    return align256((size_t)rows * n_splits * d * 4) + align256((size_t)rows * n_splits * 8);
+// Partial results of the CTAs' parts: at most one for each CTA and one more for each
+// (sequence, key head, 16 query heads).
+size_t decode_group_parts(int B, int Hkv, int G, int n_ctas) {
+    return ((size_t)n_ctas + (size_t)B * Hkv * ((G + 15) / 16)) * (G < 16 ? G : 16);
+}
+
+size_t decode_group_bytes(int B, int Hkv, int G, int n_ctas, int d) {
+    const size_t rows = decode_group_parts(B, Hkv, G, n_ctas);
+    return align256(rows * d * 4) + align256(rows * 8);
 }
 
 size_t decode_group_workspace(int B, int Hq, int Hkv, int S, int d, int window, int sinks, bool kv4) {
-    if (B < 0 || Hq < 0 || Hkv < 1 || S < 0 || d < 1 || window < 0 || sinks < 0 || Hq % Hkv) return 0;
+    if (B < 1 || Hq < 1 || Hkv < 1 || S < 0 || !valid_d(d) || window < 0 || sinks < 0 || Hq % Hkv) return 0;
     const int dev = current_device();
     const int sms = dev >= 0 && g_num_sms[dev] > 0 ? g_num_sms[dev] : 152;
-    const long long n = most_keys(S, window, sinks);
-    int splits = ba::decode_group_splits(B, Hkv, Hq / Hkv, n, kv4, sms);
-    const int other = ba::decode_group_splits(B, Hkv, Hq / Hkv, n, kv4, 152);   // before the device is known
-    if (other > splits) splits = other;
-    return decode_group_bytes((long long)B * Hq, splits, d);
+    size_t need = 0;
+    for (int n : {sms, 152})   // (before the device is known; whatever the dtype)
+        for (int dt : {BA_F32, BA_BF16}) {
+            const int ctas = ba::decode_group_ctas(B, Hkv, Hq / Hkv, most_keys(S, window, sinks), dt, d, kv4, n);
+            const size_t x = ctas < 0 ? 0 : decode_group_bytes(B, Hkv, Hq / Hkv, ctas, d);
+            if (x > need) need = x;
+        }
+    return need;
 }
 
 int check_decode_group(int B, int Hq, int Hkv, int S, int dtype, int window, int sinks, int out_dtype, float scale) {
@@ -2122,7 +2137,7 @@ int check_decode_group(int B, int Hq, int Hkv, int S, int dtype, int window, int
         return BA_ERR_ARG;
     if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return BA_ERR_SHAPE;
     if (out_dtype != BA_F32 && out_dtype != dtype) return BA_ERR_ARG;
-    if ((long long)B * Hkv > 65535 || (long long)B * Hq > 0x7fffffffLL / 128 || S > 0x7fffffff - 256)
+    if ((long long)B * Hq > 0x7fffffffLL / 256 || S > 0x7fffffff - 256)
         return BA_ERR_SHAPE;
     return BA_OK;
 }
@@ -2146,17 +2161,16 @@ int run_decode_group(ba::DecodeGroupArgs &a, const ba_tensor &q, int B, int Hq, 
     a.out = out;
     a.out_dtype = out_dtype;
     a.lse = lse;
-    const long long n = most_keys(S, window, sinks);
-    const bool kv4 = a.k_scales != nullptr;
-    a.n_splits = ba::decode_group_splits(B, Hkv, a.G, n, kv4, g_num_sms[dev]);
-    a.split_len = n > 0 ? (int)((n + a.n_splits - 1) / a.n_splits) : 1;
-    a.split_len = (a.split_len + 63) / 64 * 64;   // whole tiles for every warp
+    a.n_ctas = ba::decode_group_ctas(B, Hkv, a.G, most_keys(S, window, sinks), dtype, d, a.k_scales != nullptr,
+                                     g_num_sms[dev]);
+    if (a.n_ctas < 0) return BA_ERR_SHAPE;   // 2^31 units of 64 or 128 keys
+    a.part_rows = a.G < 16 ? a.G : 16;
     Scratch ws;
-    const int rc = ws.acquire(workspace, workspace_bytes, decode_group_bytes((long long)B * Hq, a.n_splits, d), stream);
+    const int rc = ws.acquire(workspace, workspace_bytes, decode_group_bytes(B, Hkv, a.G, a.n_ctas, d), stream);
     if (rc) return rc;
     a.part_o = static_cast<float *>(ws.ptr);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws.ptr) +
-                                           align256((size_t)B * Hq * a.n_splits * d * 4));
+                                           align256(decode_group_parts(B, Hkv, a.G, a.n_ctas) * d * 4));
     return ba::launch_decode_group(a, stream);
 }
 

@@ -5,10 +5,16 @@
 // Sequence b holds len = lengths[b] keys and its query is at position len - 1.  The
 // keys it sees, [0, s) and [lo, len) with lo = len - window behind the s = sinks first
 // ones (all of [0, len) when lo <= sinks), are numbered 0 .. n - 1 without a gap; the
-// softmax does not mind the order.  That range is cut into splits; a CTA takes one
-// split of one key head for all (up to 16) query heads that share it, so that every
-// key is read once, and each split's (O, m, l) is joined with the others' by the rule
-// of attn_merge in a second, small launch (none when there is one split).
+// softmax does not mind the order.
+//
+// Division of the work: the ranges of all (sequence, key head) pairs, cut into units of
+// one step of a CTA, lie one behind the other as one row of units, and every CTA takes
+// an equal run of it (one wave of CTAs, whatever the lengths are: they are read on the
+// device).  A run covers parts of one or more pairs; a part that is its pair's whole
+// range writes the result, any other its (O, m, l), which a second, small launch joins
+// by the rule of attn_merge.  Up to 16 query heads share the reading of their key head.
+// (Splits of a fixed length, 512 keys, took 113 us where this takes 97: 8 sequences of 32K
+// to 64K 4-bit keys, 32 query and 8 key heads, d = 128.)
 //
 // decode_mma_kernel (bf16 cache with d = 64, 128; 4-bit cache).  What bounds it is HBM:
 //   a key costs 4 G d flop for 4 d bytes (bf16) or 1.125 d bytes (4 bits), G <= 16.  On
@@ -74,7 +80,8 @@ __device__ __forceinline__ KeyRange key_range(const DecodeGroupArgs &a, int b) {
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+        // (with the hint to bring 256 bytes into L2: 64 sequences x 4K bf16 keys 208 -> 203 us)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_small(uint32_t dst, const void *src, bool in) {   // 4 or 8 bytes
@@ -167,22 +174,123 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// What a split found for element d of query head h: the reference maximum ref (log2
-// units), the sum L and the weighted sum acc relative to it.  One split: the result.
-__device__ __forceinline__ void store_split(const DecodeGroupArgs &a, int b, int h, int split, int d, float ref, float L,
-                                            float acc) {
-    const long long row = (long long)b * a.Hkv * a.G + h;
-    if (a.n_splits > 1) {
-        a.part_o[(row * a.n_splits + split) * a.d + d] = acc;
-        if (d == 0) a.part_ml[row * a.n_splits + split] = make_float2(ref, L);
+// The row of units: UNIT keys each, sequences in order, in each its HS segments (key head,
+// group of 16 query heads).  The host bounds their number below 2^31.  Every function is
+// run by whole warps.
+struct Plan {
+    int HS;      // segments per sequence
+    int total;   // units in all
+    int run;     // units per CTA
+};
+
+template <int UNIT>
+__device__ __forceinline__ int units_of(const DecodeGroupArgs &a, int b) {
+    return (key_range(a, b).n + UNIT - 1) / UNIT;
+}
+
+__device__ __forceinline__ int warp_sum(int n) { return __reduce_add_sync(0xffffffffu, n); }
+
+template <int UNIT>
+__device__ __forceinline__ Plan make_plan(const DecodeGroupArgs &a) {
+    Plan p;
+    p.HS = a.Hkv * ((a.G + 15) / 16);
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) n += units_of<UNIT>(a, b);
+    p.total = warp_sum(n) * p.HS;
+    p.run = (p.total + a.n_ctas - 1) / a.n_ctas;
+    return p;
+}
+
+// The sequence of unit u (0 <= u < total) and the first unit of that sequence.
+template <int UNIT>
+__device__ __forceinline__ void find_unit(const DecodeGroupArgs &a, const Plan &p, int u, int &b, int &base) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int v = b0 + lane < a.B ? units_of<UNIT>(a, b0 + lane) : 0;
+        int incl = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, (before + incl) * p.HS > u);
+        if (hit || b0 + 32 >= a.B) {
+            const int first = hit ? __ffs(hit) - 1 : 31;
+            b = b0 + first;
+            base = (before + __shfl_sync(0xffffffffu, incl - v, first)) * p.HS;
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// First unit of sequence b.
+template <int UNIT>
+__device__ __forceinline__ int first_unit(const DecodeGroupArgs &a, const Plan &p, int b) {
+    int n = 0;
+    for (int i = threadIdx.x & 31; i < b; i += 32) n += units_of<UNIT>(a, i);
+    return warp_sum(n) * p.HS;
+}
+
+// A part of one segment: keys [v0, v1) of sequence b for the query heads q0 .. q0 + nh - 1
+// of key head hk.  part: its place among the partial results (CTAs and segments both
+// ascend along the row, so CTA + segment is one place each), or -1 for a whole segment.
+struct Part {
+    int b, hk, q0, nh, v0, v1, part;
+};
+
+// Calls body(Part) for each part of this CTA's run.
+template <int UNIT, typename F>
+__device__ __forceinline__ void for_parts(const DecodeGroupArgs &a, F body) {
+    const Plan p = make_plan<UNIT>(a);
+    const int cta = blockIdx.x;
+    if ((long long)cta * p.run >= p.total) return;
+    int u = cta * p.run, left = min(p.run, p.total - u), b, base;
+    find_unit<UNIT>(a, p, u, b, base);
+    while (left > 0) {
+        const KeyRange kr = key_range(a, b);
+        const int per = (kr.n + UNIT - 1) / UNIT;   // units of a segment of this sequence
+        if (per > 0) {
+            const int seg = (u - base) / per, off = (u - base) - seg * per;
+            const int take = min(left, per - off);
+            Part x;
+            x.b = b;
+            const int chunks = p.HS / a.Hkv;
+            x.hk = seg / chunks;
+            const int h0 = (seg - x.hk * chunks) * 16;
+            x.q0 = x.hk * a.G + h0;
+            x.nh = min(16, a.G - h0);
+            x.v0 = off * UNIT;
+            x.v1 = min(kr.n, (off + take) * UNIT);
+            x.part = off == 0 && take == per ? -1 : cta + b * p.HS + seg;
+            body(x);
+            u += take;
+            left -= take;
+            if (seg + 1 < p.HS || off + take < per) continue;
+        }
+        base += per * p.HS;
+        ++b;
+    }
+}
+
+// What a part found for element d of its query head q0 + row: the reference maximum ref
+// (log2 units), the sum L and the weighted sum acc relative to it.
+__device__ __forceinline__ void store_part(const DecodeGroupArgs &a, const Part &x, int row, int d, float ref, float L,
+                                           float acc) {
+    if (x.part >= 0) {
+        const long long at = (long long)x.part * a.part_rows + row;
+        a.part_o[at * a.d + d] = acc;
+        if (d == 0) a.part_ml[at] = make_float2(ref, L);
         return;
     }
-    const float y = L > 0.f ? acc / L * a.out_mul : 0.f;
+    const long long at = (long long)x.b * a.Hkv * a.G + x.q0 + row;
+    const float y = L > 0.f ? acc / L * a.out_mul : (L != L ? L : 0.f);
     if (a.out_dtype == BA_BF16)
-        static_cast<__nv_bfloat16 *>(a.out)[row * a.d + d] = __float2bfloat16_rn(L != L ? L : y);
+        static_cast<__nv_bfloat16 *>(a.out)[at * a.d + d] = __float2bfloat16_rn(y);
     else
-        static_cast<float *>(a.out)[row * a.d + d] = L != L ? L : y;
-    if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (ref + log2f(L)) * LN2;
+        static_cast<float *>(a.out)[at * a.d + d] = y;
+    if (d == 0) a.lse[at] = L == 0.f ? -INFINITY : (ref + log2f(L)) * LN2;
 }
 
 // One stage of a warp's ring: SUB tiles of 16 keys, in the order in which the lanes read
@@ -197,23 +305,26 @@ struct Ring {
     static constexpr int TILE16 = K_BYTES + V_BYTES;
     static constexpr int SC_ROW = D / 16, SC_OFF = SUB * TILE16;
     static constexpr int STAGE = SC_OFF + (KV4 ? 2 * KEYS * SC_ROW : 0);
-    static constexpr int NS = 3;
+    static constexpr int NS = KV4 && D == 128 ? 2 : 3;   // (4 bits, d = 128: 3 stages 101 us, 2 stages 99 us)
     static constexpr int BYTES = DG_WARPS * NS * STAGE;
+    static constexpr int UNIT = DG_WARPS * KEYS;
 };
+
+// CTAs of a kernel that an SM holds (registers and shared memory).
+constexpr int mma_places(int d, bool kv4, int nh) {
+    return kv4 ? (d == 128 ? (nh == 1 ? 4 : 2) : (nh == 1 ? 6 : 4)) : (d == 128 ? 2 : (nh == 1 ? 4 : 4));
+}
 
 // NH: groups of 8 query heads (G <= 8 NH).
 template <int D, bool KV4, int NH>
-__global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeGroupArgs a) {
+__device__ __forceinline__ void mma_part(const DecodeGroupArgs &a, const Part &part) {
     using R = Ring<D, KV4>;
     constexpr int MT = D / 16;   // row tiles of O^T
     constexpr int KS = D / 16;   // steps of the contraction over d
     extern __shared__ __align__(128) uint8_t dg_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x, bh = blockIdx.y, b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int h0 = blockIdx.z * 16, nh = min(16, a.G - h0);   // query heads hk G + h0 .. of this CTA
+    const int b = part.b, hk = part.hk, nh = part.nh, v0 = part.v0, v1 = part.v1;
     const KeyRange kr = key_range(a, b);
-    const int v0 = split * a.split_len, v1 = min(kr.n, v0 + a.split_len);
-    if (v0 >= v1 && a.n_splits > 1) return;   // the join reads the splits that hold keys
 
     const uint32_t ring = smem_u32(dg_smem) + (uint32_t)warp * R::NS * R::STAGE;
     const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH;
@@ -235,14 +346,12 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
         else if constexpr (KV4)
             cp_small<8>(dst + lane * 8, at, in);
         else
-#pragma unroll
             for (int c = 0; c < D / 32; ++c) cp16(dst + (c * 32 + lane) * 16, at + c * 64, in);
     };
     auto copy_v = [&](uint32_t dst, const uint8_t *at, bool in) {
         if constexpr (KV4)
             cp_small<D / 16>(dst + lane * (D / 16), at, in);
         else
-#pragma unroll
             for (int c = 0; c < D / 64; ++c) cp16(dst + (c * 32 + lane) * 16, at + c * 128, in);
     };
     auto issue = [&](int i) {
@@ -310,7 +419,7 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
     for (int x = 0; x < NH; ++x) {
         const int head = g + 8 * x;
         const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (long long)b * a.qsB +
-                                  (long long)(hk * a.G + h0 + min(head, nh - 1)) * a.qsH;
+                                  (long long)(part.q0 + min(head, nh - 1)) * a.qsH;
         float mul = a.scale_log2;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -529,7 +638,6 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
         }
         __syncwarp();   // the stage may be refilled
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be placed now
     cp_wait<0>();
     __syncthreads();   // every warp is done with its ring: the merge area overlays it
 
@@ -570,12 +678,19 @@ __global__ void __launch_bounds__(DG_WARPS * 32) decode_mma_kernel(const DecodeG
                 acc += wt * mo[(w * 8 * NH + row) * D + d];
             }
         }
-        store_split(a, b, hk * a.G + h0 + row, split, d, M - (KV4 ? P_BIAS : 0.f), L, acc);
+        store_part(a, part, row, d, M - (KV4 ? P_BIAS : 0.f), L, acc);
     }
+    __syncthreads();   // the merge area becomes the next part's ring
 }
 
-// fp32 arithmetic: a group of LPK lanes owns a key, each lane 16 bytes of its row; the
-// query heads h0 .. h0 + HC - 1 share the loads.  The groups of the CTA are joined in
+template <int D, bool KV4, int NH>
+__global__ void __launch_bounds__(DG_WARPS * 32, mma_places(D, KV4, NH)) decode_mma_kernel(const DecodeGroupArgs a) {
+    for_parts<Ring<D, KV4>::UNIT>(a, [&](const Part &x) { mma_part<D, KV4, NH>(a, x); });
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be placed now
+}
+
+// fp32 arithmetic: a group of LPK lanes owns a key, each lane 16 bytes of its row; HC query
+// heads share the loads.  The groups of the CTA are joined in
 // shared memory.
 template <typename T>
 struct Row16;   // 16 bytes of T, unpacked to fp32
@@ -604,117 +719,138 @@ struct Row16<float> {
     }
 };
 
+constexpr int SIMT_UNIT = 64;
+constexpr int SIMT_PLACES = 4;
+
 template <typename T, int D, int HC>
-__global__ void __launch_bounds__(128) decode_simt_kernel(const DecodeGroupArgs a) {
+__device__ __forceinline__ void simt_part(const DecodeGroupArgs &a, const Part &part) {
     constexpr int EPL = Row16<T>::N, LPK = D / EPL, GROUPS = 128 / LPK, GPW = 32 / LPK, UN = 4;
     __shared__ float sm_o[GROUPS][HC][D];
     __shared__ float sm_m[GROUPS][HC], sm_l[GROUPS][HC];
-    const int split = blockIdx.x, bh = blockIdx.y, b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int h0 = blockIdx.z * HC, nh = min(HC, a.G - h0);
+    const int b = part.b, hk = part.hk, v0 = part.v0, v1 = part.v1;
     const KeyRange kr = key_range(a, b);
-    const int v0 = split * a.split_len, v1 = min(kr.n, v0 + a.split_len);
-    if (v0 >= v1 && a.n_splits > 1) return;
     const int grp = threadIdx.x / LPK, gl = threadIdx.x % LPK;
     const int warp = threadIdx.x / 32, gw = (threadIdx.x % 32) / LPK;
 
-    float q[HC][EPL], o[HC][EPL], m[HC], l[HC];
+    for (int h0 = 0; h0 < part.nh; h0 += HC) {   // HC query heads at a time (the next ones' keys come from L1 / L2)
+        const int nh = min(HC, part.nh - h0);
+        float q[HC][EPL], o[HC][EPL], m[HC], l[HC];
 #pragma unroll
-    for (int h = 0; h < HC; ++h) {
-        const T *qp = static_cast<const T *>(a.q) + (long long)b * a.qsB +
-                      (long long)(hk * a.G + h0 + min(h, nh - 1)) * a.qsH;
-        Row16<T>::load(qp + gl * EPL, q[h]);
-        m[h] = -INFINITY;
-        l[h] = 0.f;
+        for (int h = 0; h < HC; ++h) {
+            const T *qp = static_cast<const T *>(a.q) + (long long)b * a.qsB +
+                          (long long)(part.q0 + h0 + min(h, nh - 1)) * a.qsH;
+            Row16<T>::load(qp + gl * EPL, q[h]);
+            m[h] = -INFINITY;
+            l[h] = 0.f;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) o[h][e] = 0.f;
-    }
-    const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH + gl * 16;
-    const uint8_t *vb = static_cast<const uint8_t *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH + gl * 16;
+            for (int e = 0; e < EPL; ++e) o[h][e] = 0.f;
+        }
+        const uint8_t *kb = static_cast<const uint8_t *>(a.k) + (long long)b * a.ksB + (long long)hk * a.ksH + gl * 16;
+        const uint8_t *vb = static_cast<const uint8_t *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH + gl * 16;
 
-    // The loop runs on a warp-uniform base (the shuffles span the warp); keys behind the
-    // range are masked and their loads clamped into it.
-    for (int jb = v0 + warp * GPW * UN; jb < v1; jb += 4 * GPW * UN) {
-        const int j0 = jb + gw * UN;
-        float kx[UN][EPL], vx[UN][EPL];
+        // The loop runs on a warp-uniform base (the shuffles span the warp); keys behind the
+        // range are masked and their loads clamped into it.
+        for (int jb = v0 + warp * GPW * UN; jb < v1; jb += 4 * GPW * UN) {
+            const int j0 = jb + gw * UN;
+            float kx[UN][EPL], vx[UN][EPL];
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const long long slot = kr.slot(min(j0 + u, v1 - 1));
-            Row16<T>::load(kb + slot * a.ksT, kx[u]);
-            Row16<T>::load(vb + slot * a.vsT, vx[u]);
-            if (j0 + u >= v1) {   // a repeated key: no part of it may enter the sums
+            for (int u = 0; u < UN; ++u) {
+                const long long slot = kr.slot(min(j0 + u, v1 - 1));
+                Row16<T>::load(kb + slot * a.ksT, kx[u]);
+                Row16<T>::load(vb + slot * a.vsT, vx[u]);
+                if (j0 + u >= v1) {   // a repeated key: no part of it may enter the sums
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) vx[u][e] = 0.f;
+                    for (int e = 0; e < EPL; ++e) vx[u][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < HC; ++h) {
+                float s[UN], mx = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    float acc = 0.f;
+#pragma unroll
+                    for (int e = 0; e < EPL; ++e) acc = fmaf(q[h][e], kx[u][e], acc);
+#pragma unroll
+                    for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off, LPK);
+                    s[u] = j0 + u < v1 ? acc * a.scale_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[u]);
+                }
+                const float m_new = fmaxf(m[h], mx);
+                const float alpha = m[h] == -INFINITY ? 0.f : exp2f(m[h] - m_new);
+                l[h] *= alpha;
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) o[h][e] *= alpha;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const float p = s[u] == -INFINITY ? 0.f : exp2f(s[u] - m_new);
+                    l[h] += p;
+#pragma unroll
+                    for (int e = 0; e < EPL; ++e) o[h][e] = fmaf(p, vx[u][e], o[h][e]);
+                }
+                m[h] = m_new;
             }
         }
 #pragma unroll
         for (int h = 0; h < HC; ++h) {
-            float s[UN], mx = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                float acc = 0.f;
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) acc = fmaf(q[h][e], kx[u][e], acc);
-#pragma unroll
-                for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off, LPK);
-                s[u] = j0 + u < v1 ? acc * a.scale_log2 : -INFINITY;
-                mx = fmaxf(mx, s[u]);
-            }
-            const float m_new = fmaxf(m[h], mx);
-            const float alpha = m[h] == -INFINITY ? 0.f : exp2f(m[h] - m_new);
-            l[h] *= alpha;
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) o[h][e] *= alpha;
-#pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const float p = s[u] == -INFINITY ? 0.f : exp2f(s[u] - m_new);
-                l[h] += p;
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) o[h][e] = fmaf(p, vx[u][e], o[h][e]);
-            }
-            m[h] = m_new;
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < HC; ++h) {
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) sm_o[grp][h][gl * EPL + e] = o[h][e];
-        if (gl == 0) {
-            sm_m[grp][h] = m[h];
-            sm_l[grp][h] = l[h];
-        }
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < nh * D; x += 128) {
-        const int h = x / D, d = x % D;
-        float M = -INFINITY, L = 0.f, acc = 0.f;
-        for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, sm_m[g][h]);
-        if (M != -INFINITY) {
-            for (int g = 0; g < GROUPS; ++g) {
-                const float w = exp2f(sm_m[g][h] - M);
-                L += w * sm_l[g][h];
-                acc += w * sm_o[g][h][d];
+            for (int e = 0; e < EPL; ++e) sm_o[grp][h][gl * EPL + e] = o[h][e];
+            if (gl == 0) {
+                sm_m[grp][h] = m[h];
+                sm_l[grp][h] = l[h];
             }
         }
-        store_split(a, b, hk * a.G + h0 + h, split, d, M, L, acc);
+        __syncthreads();
+        for (int x = threadIdx.x; x < nh * D; x += 128) {
+            const int h = x / D, d = x % D;
+            float M = -INFINITY, L = 0.f, acc = 0.f;
+            for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, sm_m[g][h]);
+            if (M != -INFINITY) {
+                for (int g = 0; g < GROUPS; ++g) {
+                    const float w = exp2f(sm_m[g][h] - M);
+                    L += w * sm_l[g][h];
+                    acc += w * sm_o[g][h][d];
+                }
+            }
+            store_part(a, part, h0 + h, d, M, L, acc);
+        }
+        __syncthreads();
     }
 }
 
-// The join of a row's splits: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  One block
-// per (b, query head); it is launched while the splits still run (programmatic launch)
-// and waits for them, so that its start is hidden.
+template <typename T, int D, int HC>
+__global__ void __launch_bounds__(128) decode_simt_kernel(const DecodeGroupArgs a) {
+    for_parts<SIMT_UNIT>(a, [&](const Part &x) { simt_part<T, D, HC>(a, x); });
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The join of a row's parts: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  One block per
+// (b, query head); it is launched while the parts are still computed (programmatic
+// launch) and waits for them, so that its start is hidden.  Rows of one part are done;
+// rows without keys are written here.
+template <int UNIT>
 __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeGroupArgs a) {
     __shared__ float wt[128], red[4];
-    const int b = blockIdx.x / (a.Hkv * a.G), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int Hq = a.Hkv * a.G, b = blockIdx.x / Hq, h = blockIdx.x % Hq, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = blockIdx.x;
-    const int n = key_range(a, b).n;
-    const int used = (n + a.split_len - 1) / a.split_len;   // the splits that hold keys
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Plan p = make_plan<UNIT>(a);
+    const int per = units_of<UNIT>(a, b), hk = h / a.G, seg = hk * (p.HS / a.Hkv) + (h % a.G) / 16;
+    const int s0 = first_unit<UNIT>(a, p, b) + seg * per;
+    int c0 = 0, used = 0;
+    if (per > 0) {
+        c0 = s0 / p.run;
+        used = (s0 + per - 1) / p.run - c0 + 1;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // also where nothing is left to do: what follows
+    if (used == 1) return;                               // this launch must follow the parts' as well
     float M = -INFINITY, L = 0.f, acc = 0.f;
-    const float2 *ml = a.part_ml + row * a.n_splits;
-    const float *po = a.part_o + row * a.n_splits * a.d;
-    for (int s0 = 0; s0 < used; s0 += 128) {   // in rounds of 128 splits, carrying (M, L, acc)
-        const int here = min(128, used - s0);
-        const float2 x = threadIdx.x < here ? __ldcg(ml + s0 + threadIdx.x) : make_float2(-INFINITY, 0.f);
+    const long long first = ((long long)c0 + b * p.HS + seg) * a.part_rows + (h % a.G) % 16;
+    const float2 *ml = a.part_ml + first;
+    const float *po = a.part_o + first * a.d;
+    for (int i0 = 0; i0 < used; i0 += 128) {   // in rounds of 128 parts, carrying (M, L, acc)
+        const int here = min(128, used - i0);
+        const float2 x =
+            threadIdx.x < here ? __ldcg(ml + (long long)(i0 + threadIdx.x) * a.part_rows) : make_float2(-INFINITY, 0.f);
         float v = x.x;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
@@ -735,7 +871,8 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeGroupArgs 
         if (threadIdx.x < a.d) {
             acc *= carry;
 #pragma unroll 8
-            for (int s = 0; s < here; ++s) acc = fmaf(wt[s], __ldcg(po + (long long)(s0 + s) * a.d + threadIdx.x), acc);
+            for (int i = 0; i < here; ++i)
+                acc = fmaf(wt[i], __ldcg(po + (long long)(i0 + i) * a.part_rows * a.d + threadIdx.x), acc);
         }
         M = M_new;
     }
@@ -749,27 +886,43 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeGroupArgs 
     }
 }
 
+template <int UNIT>
+int launch_join(const DecodeGroupArgs &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.G));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<UNIT>, a) == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+}
+
 template <int D, bool KV4, int NH>
 int launch_mma(const DecodeGroupArgs &a, cudaStream_t s) {
     auto kern = decode_mma_kernel<D, KV4, NH>;
+    using R = Ring<D, KV4>;
     constexpr int merge = DG_WARPS * (8 * NH * D + 32) * 4;
-    constexpr int smem = Ring<D, KV4>::BYTES > merge ? Ring<D, KV4>::BYTES : merge;
+    constexpr int smem = R::BYTES > merge ? R::BYTES : merge;
+    static_assert(mma_places(D, KV4, NH) * (smem + 1024) <= 233472, "shared memory of an SM");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BA_ERR_CUDA;
-    kern<<<dim3(a.n_splits, a.B * a.Hkv, (a.G + 15) / 16), DG_WARPS * 32, smem, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+    kern<<<a.n_ctas, DG_WARPS * 32, smem, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return BA_ERR_CUDA;
+    return launch_join<R::UNIT>(a, s);
 }
 
 template <typename T, int D>
 int launch_simt(const DecodeGroupArgs &a, cudaStream_t s) {
-    const int hc = a.G >= 3 ? 4 : a.G;
-    const dim3 grid(a.n_splits, a.B * a.Hkv, (a.G + hc - 1) / hc);
-    if (hc == 4)
-        decode_simt_kernel<T, D, 4><<<grid, 128, 0, s>>>(a);
-    else if (hc == 2)
-        decode_simt_kernel<T, D, 2><<<grid, 128, 0, s>>>(a);
+    if (a.G >= 3)
+        decode_simt_kernel<T, D, 4><<<a.n_ctas, 128, 0, s>>>(a);
+    else if (a.G == 2)
+        decode_simt_kernel<T, D, 2><<<a.n_ctas, 128, 0, s>>>(a);
     else
-        decode_simt_kernel<T, D, 1><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+        decode_simt_kernel<T, D, 1><<<a.n_ctas, 128, 0, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return BA_ERR_CUDA;
+    return launch_join<SIMT_UNIT>(a, s);
 }
 
 template <typename T>
@@ -783,54 +936,39 @@ int launch_simt_t(const DecodeGroupArgs &a, cudaStream_t s) {
     }
 }
 
+// The tensor-core kernel's case (else the CUDA-core one).
+bool on_mma(int dtype, int d, bool kv4) { return kv4 || (dtype == BA_BF16 && (d == 64 || d == 128)); }
+
 }  // namespace
 
-// The tensor-core kernel's case (else the CUDA-core one).
-static bool on_mma(int dtype, int d, bool kv4) { return kv4 || (dtype == BA_BF16 && (d == 64 || d == 128)); }
-
-// Key splits for B * Hkv ranges of up to n_max keys.  Long ranges are cut so that the
-// launch has about eight CTAs for each place on the GPU (the last, partly filled wave is
-// then a small part) but 512 keys at least, so that joining stays small beside reading;
-// when that leaves SMs idle, down to 64 keys (a tile for each warp).
-int decode_group_splits(int B, int Hkv, int G, long long n_max, bool kv4, int num_sms) {
-    const long long bh = (long long)B * Hkv * ((G + 15) / 16);
-    if (n_max <= 64 || bh == 0) return 1;
-    const long long places = (long long)num_sms * (kv4 ? 3 : 2);
-    long long n = (n_max + 511) / 512, want = (8 * places + bh - 1) / bh;
-    if (n > want) n = want;
-    if (n * bh < num_sms) {
-        n = (n_max + 63) / 64;
-        want = (num_sms + bh - 1) / bh;
-        if (n > want) n = want;
-    }
+// CTAs of a launch over B sequences of up to n_max keys.  4 bits: one wave, so that a CTA's
+// start and its joins are paid once (8 sequences of 32K to 64K keys: 97 us; four waves of
+// shorter runs 111 us).  16 or 32 bits: up to eight waves of runs of at least 16 units,
+// because there the SMs' unequal shares of the bandwidth cost more than the starts (64
+// sequences of 4K keys: 198 us; one wave 203 us).  At least a CTA for each SM, when there
+// are units for them: a single sequence is bound by the time of one run.
+int decode_group_ctas(int B, int Hkv, int G, long long n_max, int dtype, int d, bool kv4, int num_sms) {
+    const bool mma = on_mma(dtype, d, kv4);
+    const int unit = mma ? (kv4 ? Ring<128, true>::UNIT : Ring<128, false>::UNIT) : SIMT_UNIT;
+    const long long units = (long long)B * Hkv * ((G + 15) / 16) * ((n_max + unit - 1) / unit);
+    if (units > 0x7fffffffLL - 0x10000) return -1;
+    const long long most = (long long)(kv4 ? 1 : 8) * num_sms * (mma ? mma_places(d, kv4, G > 8 ? 2 : 1) : SIMT_PLACES);
+    long long n = units / (kv4 ? 4 : 16);
+    if (n > most) n = most;
+    if (n < num_sms) n = units < num_sms ? units : num_sms;
     return (int)(n < 1 ? 1 : n);
 }
 
 int launch_decode_group(const DecodeGroupArgs &a, cudaStream_t s) {
     const bool kv4 = a.k_scales != nullptr;
-    int rc;
-    if (on_mma(a.dtype, a.d, kv4)) {
-        const bool two = a.G > 8;
-        if (kv4)
-            rc = a.d == 128 ? (two ? launch_mma<128, true, 2>(a, s) : launch_mma<128, true, 1>(a, s))
-                            : (two ? launch_mma<64, true, 2>(a, s) : launch_mma<64, true, 1>(a, s));
-        else
-            rc = a.d == 128 ? (two ? launch_mma<128, false, 2>(a, s) : launch_mma<128, false, 1>(a, s))
-                            : (two ? launch_mma<64, false, 2>(a, s) : launch_mma<64, false, 1>(a, s));
-    } else {
-        rc = a.dtype == BA_BF16 ? launch_simt_t<__nv_bfloat16>(a, s) : launch_simt_t<float>(a, s);
-    }
-    if (rc || a.n_splits == 1) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.G));
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel, a) == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+    if (!on_mma(a.dtype, a.d, kv4))
+        return a.dtype == BA_BF16 ? launch_simt_t<__nv_bfloat16>(a, s) : launch_simt_t<float>(a, s);
+    const bool two = a.G > 8;
+    if (kv4)
+        return a.d == 128 ? (two ? launch_mma<128, true, 2>(a, s) : launch_mma<128, true, 1>(a, s))
+                          : (two ? launch_mma<64, true, 2>(a, s) : launch_mma<64, true, 1>(a, s));
+    return a.d == 128 ? (two ? launch_mma<128, false, 2>(a, s) : launch_mma<128, false, 1>(a, s))
+                      : (two ? launch_mma<64, false, 2>(a, s) : launch_mma<64, false, 1>(a, s));
 }
 
 }  // namespace ba

@@ -125,15 +125,16 @@ struct DecodeGroupArgs {
     int window, sinks;                   // window 0: every key
     float scale_log2;                    // softmax scale * log2(e) (times the 4-bit keys' power of two)
     float out_mul;                       // factor of the outputs (the 4-bit values' power of two)
-    int split_len, n_splits;
-    float *part_o;                       // (B Hq, n_splits, d) weighted sums
-    float2 *part_ml;                     // (B Hq, n_splits) reference maximum (log2 units) and sum
+    int n_ctas;                          // CTAs that share the work
+    int part_rows;                       // query heads of a part: min(G, 16)
+    float *part_o;                       // (n_ctas + segments, part_rows, d) weighted sums
+    float2 *part_ml;                     // (n_ctas + segments, part_rows) reference maximum (log2 units) and sum
     void *out;                           // (B, Hq, 1, d) contiguous, out_dtype
     int out_dtype;
     float *lse;                          // (B, Hq, 1)
 };
 
-int decode_group_splits(int B, int Hkv, int G, long long n_max, bool kv4, int num_sms);
+int decode_group_ctas(int B, int Hkv, int G, long long n_max, int dtype, int d, bool kv4, int num_sms);
 int launch_decode_group(const DecodeGroupArgs &a, cudaStream_t s);
 
 // Writing and reading a cache held in 4 bits.

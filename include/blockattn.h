@@ -297,14 +297,15 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok,
  *  scale: > 0, or <= 0 for 1/sqrt(d).
  *  out: (B, Hq, Lq, d) contiguous, 16-byte aligned, out_dtype = BA_F32 or dtype;
  *    lse: (B, Hq, Lq) fp32.  A row that sees no key gets out = 0, lse = -inf.
- *  workspace: attn_window_fwd_workspace_size() bytes.
+ *  workspace: attn_window_fwd_workspace_size() bytes (0 for launches of no more work
+ *    items than SMs).
  * The walk of a query tile is its window and the sinks: the cost is that of
  * window + sinks keys a row, whatever the length.
  * Errors: BA_ERR_ARG (NULL pointers, negative sizes, window < 1, a mask that does
  * not cover Lk keys, a misaligned out), BA_ERR_SHAPE (d, Hq not a multiple of Hkv,
  * positions of 2^31 and beyond).
  */
-size_t attn_window_fwd_workspace_size(void);
+size_t attn_window_fwd_workspace_size(int B, int Hq, int Lq, int d, int dtype);
 int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v,
                     int B, int Hq, int Hkv, int Lq, int Lk, int d, int dtype,
                     int64_t q_off, int window, int sinks,
