@@ -22,7 +22,7 @@ _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_BUILD, "libblockattn.so")
 _SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu",
-            "decode_group.cu", "kv4.cu", "qk_norm.cu"]
+            "decode_group.cu", "kv4.cu", "qk_norm.cu", "attn_window_simt.cu"]
 _HEADERS = ["common.cuh", "internal.h", "epilogue.cuh", "tc_ptx.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

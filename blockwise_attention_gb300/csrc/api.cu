@@ -1904,7 +1904,7 @@ int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hk
     a.err = g_err_ptr[dev];
     a.wait_limit_ns = kWaitLimitNs;
     if (!tc_supported(dtype, d) || Lk == 0 || !tma_ok(q, B, Hq) || !tma_ok(k, B, Hkv) || !tma_ok(v, B, Hkv))
-        return launch_attn_simt(a, stream);
+        return launch_window_simt(a, stream);
     if ((rc = get_encoder())) return rc;
     // With no more items than SMs every CTA takes one: dealt round-robin, without the
     // counter and the launch that clears it.

@@ -34,9 +34,8 @@ __global__ void __launch_bounds__(TILE) attn_simt_kernel(const AttnArgs a) {
     const bool valid = r < qt.len;
     const long long qpos = qt.pos0 + r;
     const Tin *qb = static_cast<const Tin *>(a.q) + qt.b * a.qsB + qt.h * a.qsH;
-    const int kvh = S == WALK_WINDOW ? qt.h / g.kv_group : qt.h;
-    const Tin *kb = static_cast<const Tin *>(a.k) + qt.b * a.ksB + kvh * a.ksH;
-    const Tin *vb = static_cast<const Tin *>(a.v) + qt.b * a.vsB + kvh * a.vsH;
+    const Tin *kb = static_cast<const Tin *>(a.k) + qt.b * a.ksB + qt.h * a.ksH;
+    const Tin *vb = static_cast<const Tin *>(a.v) + qt.b * a.vsB + qt.h * a.vsH;
 
     float q[D], o[D];
 #pragma unroll
@@ -57,7 +56,6 @@ __global__ void __launch_bounds__(TILE) attn_simt_kernel(const AttnArgs a) {
                 bool in = s0 + j < kt.len;
                 const long long row = row_token<S>(g, kt.row0 + s0 + j);
                 Ks[j][c] = in ? to_f32(kb[row * a.ksT + c]) : 0.f;
-                if (S == WALK_WINDOW && in && g.kpm && g.kpm[qt.b * g.kpm_ld + row]) in = false;   // a padded key's V may hold anything
                 Vs[j][c] = in ? to_f32(vb[row * a.vsT + c]) : 0.f;
             }
             __syncthreads();
@@ -68,7 +66,7 @@ __global__ void __launch_bounds__(TILE) attn_simt_kernel(const AttnArgs a) {
             for (int j = 0; j < SUB; ++j) {
                 int kj = s0 + j;
                 bool ok = kj < kt.len &&
-                          (kt.cls == BA_TILE_FULL || !excluded<S>(g, qt.b, qpos, kt.pos0 + kj));
+                          (kt.cls == BA_TILE_FULL || !excluded(g, qt.b, qpos, kt.pos0 + kj));
                 float dot = 0.f;
 #pragma unroll
                 for (int c = 0; c < D; ++c) dot = fmaf(q[c], Ks[j][c], dot);
@@ -114,7 +112,6 @@ int launch_ds(const AttnArgs &a, cudaStream_t s) {
 
 template <int D>
 int launch_d(const AttnArgs &a, cudaStream_t s) {
-    if (a.g.window > 0) return launch_ds<D, WALK_WINDOW>(a, s);
     return a.g.striped ? launch_ds<D, WALK_STRIPED>(a, s) : launch_ds<D, WALK_PLAIN>(a, s);
 }
 

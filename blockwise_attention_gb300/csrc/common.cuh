@@ -278,11 +278,6 @@ __host__ __device__ __forceinline__ bool kwalk_next(const Geom &g, const QTile &
         k.idx = w.idx;
         w.row = row + TILE;
         ++w.idx;
-        if constexpr (S == WALK_WINDOW) {
-            k.cls = window_class(g, w.q_first, w.q_last, pos, pos + k.len - 1);
-            if (k.cls == BA_TILE_FULL && g.kpm) k.cls = BA_TILE_PARTIAL;
-            return true;
-        }
         if (g.cls) {
             k.cls = g.cls[((long long)q.b * g.n_qtiles + q.g) * g.n_ktiles + k.idx];
             if (k.cls == BA_TILE_EMPTY) continue;
@@ -374,10 +369,8 @@ __host__ __device__ inline QTile work_item(const Geom &g, int w) {
 }
 
 // Is key position kp excluded for query position qp of batch item b?
-template <int S = WALK_PLAIN>
 __device__ inline bool excluded(const Geom &g, int b, long long qp, long long kp) {
     if (g.causal && kp > qp) return true;
-    if (S == WALK_WINDOW && kp <= qp - g.window && kp >= g.sinks) return true;
     if (g.kpm && g.kpm[b * g.kpm_ld + kp]) return true;
     if (g.am && g.am[qp * g.am_ld + kp]) return true;
     return false;

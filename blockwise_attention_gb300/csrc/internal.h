@@ -183,6 +183,7 @@ struct TmaMaps {
 };
 
 int launch_attn_simt(const AttnArgs &a, cudaStream_t s);
+int launch_window_simt(const AttnArgs &a, cudaStream_t s);
 int launch_attn_tc(const AttnArgs &a, const TmaMaps &maps, int num_sms, cudaStream_t s);
 bool tc_supported(int dtype, int d);
 size_t tc_smem_bytes(int d);
