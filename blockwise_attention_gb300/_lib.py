@@ -561,9 +561,9 @@ def _empty(ref, shape, dtype, stream):
     """A new tensor beside ref, from the memory of the stream that the call runs on (so that
     nothing still pending on another stream uses the memory, and its reuse waits for this call)."""
     if stream is None:
-        return ref.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=ref.device)   # (ref.new_empty takes 1 us more)
     with torch.cuda.stream(stream):
-        return ref.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=ref.device)
 
 
 def _buffer(ref, name, t, shape, dtype, stream):
@@ -575,11 +575,19 @@ def _buffer(ref, name, t, shape, dtype, stream):
     return t
 
 
-def _out_pair(q, out, out_dtype, lse, stream):
-    """out and lse of an attention call on q."""
+def _out_pair(q, shape, out, out_dtype, lse, stream):
+    """out and lse of an attention call on q of the given shape, and out's dtype code."""
     if out_dtype is None:
         out_dtype = q.dtype if out is None else out.dtype
-    return _buffer(q, "out", out, q.shape, out_dtype, stream), _buffer(q, "lse", lse, q.shape[:3], torch.float32, stream)
+    code = _DTYPES.get(out_dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    if out is None and lse is None and stream is None:
+        dev = q.device
+        return (torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape[:3], dtype=torch.float32, device=dev),
+                code)
+    return (_buffer(q, "out", out, shape, out_dtype, stream), _buffer(q, "lse", lse, shape[:3], torch.float32, stream),
+            code)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -600,10 +608,9 @@ def _scratch(ref, need, workspace, stream):
 
 
 def _c_int(name, x, lo):
-    x = int(x)
-    if not lo <= x < 1 << 31:
-        raise ValueError(f"{name} = {x} is not in [{lo}, 2^31)")
-    return x
+    if not lo <= x < 2147483648 or int(x) != x:
+        raise ValueError(f"{name} = {x} is not an integer in [{lo}, 2^31)")
+    return int(x)
 
 
 def attn_window_fwd(q, k, v, *, window, sinks=0, q_off=0, key_padding_mask=None, scale=None, out=None, out_dtype=None,
@@ -616,12 +623,12 @@ def attn_window_fwd(q, k, v, *, window, sinks=0, q_off=0, key_padding_mask=None,
     window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
     dt = _code(q.dtype)
     dev = _device(q, k=k, v=v, key_padding_mask=key_padding_mask)
-    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    out, lse, odt = _out_pair(q, (B, Hq, Lq, d), out, out_dtype, lse, stream)
     kpm, kpm_ld = _mask(key_padding_mask, B, Lk, "key_padding_mask")
     need = _workspace_bytes("attn_window_fwd_workspace_size", dev, B, Hq, Lq, d, dt)
     ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
     rc = lib.attn_window_fwd(_view("q", q), _view("k", k), _view("v", v), B, Hq, Hkv, Lq, Lk, d, dt, q_off, window, sinks,
-                             kpm, kpm_ld, 0.0 if scale is None else float(scale), out.data_ptr(), _code(out.dtype),
+                             kpm, kpm_ld, 0.0 if scale is None else float(scale), out.data_ptr(), odt,
                              lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_window_fwd", rc)
     return out, lse
@@ -705,12 +712,12 @@ def attn_window_decode_fwd(q, k_cache, v_cache, *, window, sinks=0, lengths=None
     dt = _code(q.dtype)
     dev = _device(q, k_cache=k_cache, v_cache=v_cache)
     lens = _per_sequence("lengths", lengths, B, dev)
-    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    out, lse, odt = _out_pair(q, (B, Hq, 1, d), out, out_dtype, lse, stream)
     need = _workspace_bytes("attn_window_decode_workspace_size", dev, B, Hq, Hkv, S, d, window, sinks)
     ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
     rc = lib.attn_window_decode_fwd(_view("q", q), _view("k_cache", k_cache), _view("v_cache", v_cache), B, Hq, Hkv, S, d,
                                     dt, lens, window, sinks, 0.0 if scale is None else float(scale), out.data_ptr(),
-                                    _code(out.dtype), lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
+                                    odt, lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_window_decode_fwd", rc)
     return out, lse
 
@@ -785,18 +792,18 @@ def attn_decode_kv4_fwd(q, cache, *, lengths=None, window=0, sinks=0, scale=None
     every key (window = 0) or a window with sinks; see include/blockattn.h.  Returns (out, lse)."""
     lib = load()
     B, Hkv, S, d = cache.shape
-    shape = q.shape
+    shape = tuple(q.shape)
     if len(shape) != 4 or shape[0] != B or shape[2] != 1 or shape[3] != d or Hkv == 0 or shape[1] % Hkv:
         raise ValueError(f"q of shape {tuple(shape)} does not match a cache of {cache.shape}")
     Hq = shape[1]
     window, sinks = _c_int("window", window, 0), _c_int("sinks", sinks, 0)
     dev = _device(q, cache=cache.k_codes)
     lens = _per_sequence("lengths", lengths, B, dev)
-    out, lse = _out_pair(q, out, out_dtype, lse, stream)
+    out, lse, odt = _out_pair(q, (B, Hq, 1, d), out, out_dtype, lse, stream)
     need = _workspace_bytes("attn_decode_kv4_workspace_size", dev, B, Hq, Hkv, S, d, window, sinks)
     ws, ws_bytes, keep = _scratch(q, need, workspace, stream)
     rc = lib.attn_decode_kv4_fwd(_view("q", q), cache._c, B, Hq, Hkv, S, d, _code(q.dtype), lens, window, sinks,
-                                 0.0 if scale is None else float(scale), out.data_ptr(), _code(out.dtype),
+                                 0.0 if scale is None else float(scale), out.data_ptr(), odt,
                                  lse.data_ptr(), ws, ws_bytes, _on_stream(stream, dev))
     _check("attn_decode_kv4_fwd", rc)
     return out, lse

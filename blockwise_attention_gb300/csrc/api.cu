@@ -1668,7 +1668,7 @@ int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, co
                  float pos_scale, void *yq, void *yk, bool &vec) {
     std::memset(&a, 0, sizeof a);
     if (B < 0 || Hq < 0 || Hkv < 0 || T < 0 || !valid_dtype(dtype) || !(eps >= 0.f) || !(base > 0.f) ||
-        !(pos_scale >= 0.f) || positions_ld < 0)
+        !(pos_scale >= 0.f) || !std::isfinite(pos_scale) || !std::isfinite(base) || positions_ld < 0)
         return BA_ERR_ARG;
     if (w_dtype != BA_F32 && w_dtype != dtype) return BA_ERR_ARG;
     if (!valid_d(d)) return BA_ERR_SHAPE;
@@ -1701,9 +1701,11 @@ int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, co
     a.eps = eps;
     a.positions = positions;
     a.pos_ld = positions_ld;
-    a.pos_scale = pos_scale > 0.f ? (double)pos_scale : 1.0;
-    for (int c = 0; c < d / 2; ++c)
-        a.turn[c] = std::pow((double)base, -(double)(2 * c) / (double)d) / 6.283185307179586476925286766559;
+    for (int c = 0; c < d / 2; ++c) {
+        const double turn = std::pow((double)base, -(double)(2 * c) / (double)d) *
+                            (pos_scale > 0.f ? (double)pos_scale : 1.0) / 6.283185307179586476925286766559;
+        a.turn[c] = (unsigned long long)((turn - std::floor(turn)) * 0x1p64);   // (whole turns do not matter: m is an integer)
+    }
     const bool own = positions && positions_ld > 0;   // each sequence has its own positions
     a.places = own ? (long long)B * T : T;
     a.nb = own ? 1 : B;
@@ -2311,7 +2313,7 @@ int kv4_append(ba_tensor k, ba_tensor v, ba_kv4 cache, int B, int H, int T, int 
     a.start = start;
     a.counts = counts;
     kv4_args(a, cache);
-    return ba::launch_kv4_append(a, g_num_sms[dev], stream);
+    return ba::launch_kv4_append(a, stream);
 }
 
 int kv4_read(ba_kv4 cache, int B, int H, int S, int d, int first, int T, int dtype, void *k, void *v,
@@ -2338,7 +2340,7 @@ int kv4_read(ba_kv4 cache, int B, int H, int S, int d, int first, int T, int dty
     a.y[0] = k;
     a.y[1] = v;
     kv4_args(a, cache);
-    return ba::launch_kv4_read(a, g_num_sms[dev], stream);
+    return ba::launch_kv4_read(a, stream);
 }
 
 // Same work as attn_block_fwd, with the tile-class map in the library's fixed

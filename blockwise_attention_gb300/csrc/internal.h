@@ -151,8 +151,8 @@ struct Kv4Args {
     int exp[2];                          // a stored value is code * scale * 2^exp
 };
 
-int launch_kv4_append(const Kv4Args &a, int num_sms, cudaStream_t s);
-int launch_kv4_read(const Kv4Args &a, int num_sms, cudaStream_t s);
+int launch_kv4_append(const Kv4Args &a, cudaStream_t s);
+int launch_kv4_read(const Kv4Args &a, cudaStream_t s);
 
 // Norm per head and rotation of queries ([0]) and keys ([1]), forward or backward.
 struct QkNormArgs {
@@ -165,15 +165,16 @@ struct QkNormArgs {
     void *y[2];                          // y, or dx: contiguous (B, H, T, d)
     const int32_t *positions;            // nullptr: t
     long long pos_ld;                    // entries between sequences (0: shared)
-    double pos_scale, turn[64];          // turn[c] = base^(-2c/d) / (2 pi)
+    unsigned long long turn[64];         // pos_scale base^(-2c/d) / (2 pi), its fraction times 2^64
     float eps;
     long long places;                    // T, or B T when each sequence has its own positions
     int nb;                              // sequences of a place: B, or 1
+    int splits;                          // CTAs that share the rows of a block of places
     float *part;                         // backward: (blocks, 2, d) sums of dz n
 };
 
 void qk_norm_grid(long long places, int rows, int d, int dtype, int num_sms, int &gx, int &gy);
-int launch_qk_norm(const QkNormArgs &a, bool bwd, int g_dtype, bool vec, int num_sms, float *dwq, float *dwk,
+int launch_qk_norm(QkNormArgs a, bool bwd, int g_dtype, bool vec, int num_sms, float *dwq, float *dwk,
                    cudaStream_t s);
 
 // TMA descriptors of Q, K, V (loads) and out (stores, boxes of 32 rows) for

@@ -91,12 +91,15 @@ def test_values_at_and_next_to_every_border(dt):
     assert torch.equal(ba.kv4_read(cache, x.shape[2], dtype=torch.float32)[0].double(), val)
 
 
-def test_not_finite_values_saturate():
-    x = rand((1, 1, 3, 64), torch.float32, 3)
+@pytest.mark.parametrize("exp", [0, -100, 100, -3])
+def test_not_finite_and_huge_values_saturate(exp):
+    x = rand((1, 1, 5, 64), torch.float32, 3) * 2.0 ** exp
     x[0, 0, 0, 5], x[0, 0, 1, 20], x[0, 0, 2, 40] = math.inf, -math.inf, math.nan
-    cache = ba.KV4Cache.empty(1, 1, 3, 64)
+    x[0, 0, 3, 7], x[0, 0, 3, 33] = -3.4e38, 3.4e38
+    x[0, 0, 4] *= -1e4
+    cache = ba.KV4Cache.empty(1, 1, 5, 64, k_exp=exp, v_exp=exp)
     ba.kv4_append(cache, x, x)
-    assert torch.equal(ba.kv4_read(cache, 3, dtype=torch.float32)[1].double(), quantise(x, 0)[2])
+    assert torch.equal(ba.kv4_read(cache, 5, dtype=torch.float32)[1].double(), quantise(x, exp)[2])
 
 
 def test_append_starts_counts_and_leaves_the_rest():

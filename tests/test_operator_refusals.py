@@ -120,7 +120,7 @@ def test_qk_norm():
         return lib.qk_norm_rope_fwd(q, k, w, w, wdt, B, Hq, Hkv, T, d, dt, eps, None, ld, base, ps, y, y, None)
     nan = float("nan")
     for bad in (dict(q=NONE), dict(k=NONE), dict(w=None), dict(y=None), dict(y=ctypes.c_void_p((1 << 20) + 8)), dict(wdt=4),
-                dict(dt=F32, wdt=BF), dict(eps=-1.0), dict(eps=nan), dict(base=0.0), dict(base=nan), dict(ps=-1.0), dict(T=-1),
+                dict(dt=F32, wdt=BF), dict(eps=-1.0), dict(eps=nan), dict(base=0.0), dict(base=nan), dict(base=float("inf")), dict(ps=-1.0), dict(ps=float("inf")), dict(T=-1),
                 dict(ld=-1)):
         assert run(**bad) == BA_ERR_ARG, bad
     assert run(d=96) == BA_ERR_SHAPE and run(T=0) == BA_OK and run(Hq=0, Hkv=0) == BA_OK
