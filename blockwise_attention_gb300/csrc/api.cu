@@ -1713,9 +1713,9 @@ int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, co
 }
 
 size_t qk_norm_bytes(int B, int Hq, int Hkv, int T, int d, int dtype, bool own, int num_sms) {
-    int gx, gy;
-    ba::qk_norm_grid(own ? (long long)B * T : T, (own ? 1 : B) * (Hq + Hkv), d, dtype, num_sms, gx, gy);
-    return align256((size_t)gx * gy * 2 * d * 4);
+    int ctas, run;
+    ba::qk_norm_grid(own ? (long long)B * T : T, (own ? 1 : B) * (Hq + Hkv), d, dtype, num_sms, ctas, run);
+    return align256((size_t)ctas * 2 * d * 4);
 }
 
 }  // namespace

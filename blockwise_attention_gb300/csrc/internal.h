@@ -169,11 +169,11 @@ struct QkNormArgs {
     float eps;
     long long places;                    // T, or B T when each sequence has its own positions
     int nb;                              // sequences of a place: B, or 1
-    int splits;                          // CTAs that share the rows of a block of places
+    int run;                             // rows of blocks of places per CTA
     float *part;                         // backward: (blocks, 2, d) sums of dz n
 };
 
-void qk_norm_grid(long long places, int rows, int d, int dtype, int num_sms, int &gx, int &gy);
+void qk_norm_grid(long long places, int rows, int d, int dtype, int num_sms, int &ctas, int &run);
 int launch_qk_norm(QkNormArgs a, bool bwd, int g_dtype, bool vec, int num_sms, float *dwq, float *dwk,
                    cudaStream_t s);
 
