@@ -322,12 +322,14 @@ __device__ __forceinline__ uint32_t window_bits_queries(const BwdArgs &a, long l
 }
 
 // The query at position qp against the keys k0 + i, i < 32, of which the first n exist.
-__device__ __noinline__ uint32_t window_bits_keys(const BwdArgs &a, int b, long long qp, long long k0, int n) {
+// Called by whole warps: the padding is the same for every query, a lane reads one key's.
+__device__ __forceinline__ uint32_t window_bits_keys(const BwdArgs &a, int b, long long qp, long long k0, int n) {
     uint32_t m = low_bits(min((long long)n, qp - k0 + 1));
     m &= ~low_bits(qp - a.window + 1 - k0) | low_bits(a.sinks - k0);
-    if (a.kpm)
-        for (int i = 0; i < 32 && i < n; ++i)
-            if (a.kpm[b * a.kpm_ld + k0 + i]) m &= ~(1u << i);
+    if (a.kpm) {
+        const int lane = threadIdx.x & 31;
+        m &= ~__ballot_sync(0xffffffffu, lane < n && a.kpm[b * a.kpm_ld + k0 + lane]);
+    }
     return m;
 }
 
@@ -1108,10 +1110,15 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_ld32(tmem + lane_addr + C::S_COL + c * 32, rs);
                     tmem_ld32(tmem + lane_addr + C::DP_COL + c * 32, rd);
                     tmem_wait_ld();
-                    const uint32_t keep =
-                        full ? 0xffffffffu
-                        : W  ? (ivalid ? window_bits_keys(a, b, qp, pt.pos0 + c * 32, pt.len - c * 32) : 0u)
-                             : keep_bits_keys(a, b, qp, ivalid, pt.pos0 + c * 32, pt.len - c * 32);
+                    uint32_t keep = 0xffffffffu;
+                    if (!full) {   // (the same for the whole warp)
+                        if constexpr (W) {
+                            const uint32_t seen = window_bits_keys(a, b, qp, pt.pos0 + c * 32, pt.len - c * 32);
+                            keep = ivalid ? seen : 0u;
+                        } else {
+                            keep = keep_bits_keys(a, b, qp, ivalid, pt.pos0 + c * 32, pt.len - c * 32);
+                        }
+                    }
                     uint32_t pd[16];
 #pragma unroll
                     for (int k2 = 0; k2 < 16; ++k2) {
@@ -1220,7 +1227,7 @@ int launch_attn_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStre
 // sink tiles' partials.
 int launch_attn_window_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s) {
     if ((long long)a.B * a.H == 0) return BA_OK;
-    int rc = launch_bwd_pre(a, num_sms, s);
+    int rc = launch_window_pre(a, num_sms, s);
     if (rc) return rc;
     if (a.d == 128)
         rc = launch_bwd_tc_d<128, true>(a, m, num_sms, s);

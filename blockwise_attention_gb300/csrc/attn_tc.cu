@@ -163,7 +163,6 @@ struct Keep4 {
     uint32_t m[4];
 };
 
-template <int S>
 __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, bool row_valid, long long kpos0,
                                          int klen) {
     Keep4 r;
@@ -175,13 +174,6 @@ __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, b
             const long long lim = qpos - kpos0 - 32 * c;   // key 32 c + i lies in the future when i > lim
             if (lim < 0) m = 0u;
             else if (lim < 31) m &= (2u << lim) - 1u;
-        }
-        if constexpr (S == WALK_WINDOW) {
-            const long long lo = qpos - g.window + 1 - kpos0 - 32 * c;   // first key of the window
-            const long long ns = g.sinks - kpos0 - 32 * c;               // sink keys of this word
-            const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : ~((1u << lo) - 1u));
-            const uint32_t snk = ns >= 32 ? 0xffffffffu : (ns > 0 ? (1u << ns) - 1u : 0u);
-            m &= win | snk;
         }
         r.m[c] = m;
     }
@@ -201,6 +193,31 @@ __device__ __noinline__ Keep4 keep_bits4(const Geom &g, int b, long long qpos, b
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) r.m[c] &= ~(ek[c] | ea[c]);
+    return r;
+}
+
+// The same under the window.
+// The padding is the same for every row: each lane reads four keys' bytes and the warp
+// shares them (rows reading 128 bytes each: 1001-token training step, padded, 41 us of it).
+// Called by whole warps.
+__device__ __noinline__ Keep4 keep_bits4_window(const Geom &g, int b, int qpos, int k0, int klen) {
+    Keep4 r;
+    // keys [max(window's first, 0), up) and [0, min(sinks, up)) of the tile, up behind the
+    // row's own position; positions fit 32 bits
+    const int up = min(klen, qpos - k0 + 1);
+    const int first = max(qpos - g.window + 1 - k0, 0), ns = min(max(g.sinks - k0, 0), klen);
+    auto low = [](int n) { return n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u); };
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.m[c] = low(up - 32 * c) & (~low(first - 32 * c) | low(ns - 32 * c));
+    if (g.kpm) {
+        const int lane = threadIdx.x & 31;
+        const uint8_t *p = g.kpm + b * g.kpm_ld + k0 + lane;
+        bool e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) e[c] = 32 * c + lane < klen && __ldg(p + 32 * c) != 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) r.m[c] &= ~__ballot_sync(0xffffffffu, e[c]);
+    }
     return r;
 }
 
@@ -620,7 +637,12 @@ __global__ void __launch_bounds__(320, 1)
                 }
                 Keep4 keep;
                 if constexpr (PF) {
-                    if (masked) keep = keep_bits4<S>(g, qt.b, qpos, row < qt.len, kt.pos0, kt.len);
+                    if (masked) {
+                        if constexpr (S == WALK_WINDOW)
+                            keep = keep_bits4_window(g, qt.b, (int)qpos, (int)kt.pos0, kt.len);
+                        else
+                            keep = keep_bits4(g, qt.b, qpos, row < qt.len, kt.pos0, kt.len);
+                    }
                 }
                 if (!warp_wait(bar(C::B_SFULL + x), sx & 1, abort, a.err, lim)) {
                     ok = false;

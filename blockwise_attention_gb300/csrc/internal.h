@@ -78,6 +78,7 @@ int launch_attn_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_bwd_pre(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_attn_window_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_attn_window_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s);
+int launch_window_pre(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_sink_sum(const BwdArgs &a, int tile_rows, int num_sms, cudaStream_t s);
 bool bwd_tc_supported(int dtype, int d);
 int launch_attn_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s);

@@ -19,7 +19,7 @@
 // SM has few; then sincospi in fp32.  (Product and reduction in fp64, and one block of
 // positions a CTA: 8K positions, 2 sequences, 20 heads, forward 54 us.)
 // dw: every block writes its sums, a second launch adds the blocks' in a fixed order (no
-// atomics), in fp64.
+// atomics).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -339,30 +339,33 @@ __global__ void __launch_bounds__(QN_THREADS, 3) qk_norm_kernel(const QkNormArgs
     }
 }
 
-// dw[j] = the sum of the blocks' partials of column j in fp64: 32 columns a block, 32 runs of
-// blocks beside each other with eight loads in flight each (one run of 8 warps, a load at a
-// time, took as long as a fifth of the gradients), joined in a fixed order.
+// dw[j] = the sum of the blocks' partials of column j, in a fixed order: 32 columns a block,
+// 32 runs of blocks beside each other with eight loads in flight each, then the runs.  In
+// fp32: a column's chain is n_blocks / 32 + 32 additions of partials that are sums
+// themselves (in fp64, of which an SM has few units: 13 us).
 __global__ void __launch_bounds__(1024) qk_norm_sum_kernel(const float *part, int n_blocks, int d, float *dwq, float *dwk) {
-    __shared__ double sm[32][33];
+    __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
-    double v = 0.0;
+    float v = 0.f;
     if (j < 2 * d) {
         const float *p = part + j;
         for (int b0 = run; b0 < n_blocks; b0 += 256) {
             float x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = b0 + 32 * k < n_blocks ? __ldcg(p + (long long)(b0 + 32 * k) * 2 * d) : 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v += (double)x[k];
+            v += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
         }
     }
     sm[run][lane] = v;
     __syncthreads();
-    if (run == 0 && j < 2 * d) {
+    // warp `run` joins column `run`: its lanes the runs
+    v = sm[lane][run];
 #pragma unroll
-        for (int k = 1; k < 32; ++k) v += sm[k][lane];
-        float *dst = j < d ? dwq : dwk;
-        if (dst) dst[j < d ? j : j - d] = (float)v;
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const int c = blockIdx.x * 32 + run;
+    if (lane == 0 && c < 2 * d) {
+        float *dst = c < d ? dwq : dwk;
+        if (dst) dst[c < d ? c : c - d] = v;
     }
 }
 
