@@ -729,24 +729,24 @@ class KV4Cache:
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_exp", "v_exp", "shape", "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_exp=0, v_exp=0):
-        codes, scales = (k_codes, v_codes), (k_scales, v_scales)
-        for t in codes + scales:
-            if t.dtype != torch.uint8 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda or t.device != k_codes.device:
-                raise ValueError("codes and scales are 4-D uint8 CUDA tensors on one device with a contiguous last axis")
-        B, H, S, half = k_codes.shape
-        if half not in (32, 64):
+        dev = k_codes.get_device()
+        for t in (k_codes, k_scales, v_codes, v_scales):
+            if t.dtype != torch.uint8 or t.dim() != 4 or t.get_device() != dev or dev < 0:
+                raise ValueError("codes and scales are 4-D uint8 CUDA tensors on one device")
+        B, H, S, half = shape = k_codes.shape
+        cs, ss = k_codes.stride(), k_scales.stride()
+        if half != 64 and half != 32:
             raise ValueError(f"codes of {half} bytes a row: rows of d = 64 or 128 values take 32 or 64")
-        if v_codes.shape != k_codes.shape or any(tuple(t.shape) != (B, H, S, half // 8) for t in scales):
+        if v_codes.shape != shape or k_scales.shape != (B, H, S, half // 8) or v_scales.shape != k_scales.shape:
             raise ValueError("codes (B, H, S, d / 2) and scales (B, H, S, d / 16) of K and V must match")
-        if k_codes.stride() != v_codes.stride() or k_scales.stride() != v_scales.stride():
-            raise ValueError("K and V must have the same strides")
-        for e in (k_exp, v_exp):
-            if int(e) != e or not -100 <= e <= 100:
-                raise ValueError(f"exponent {e} is not an integer in [-100, 100]")
+        if v_codes.stride() != cs or v_scales.stride() != ss or cs[3] != 1 or ss[3] != 1:
+            raise ValueError("K and V must have the same strides, and contiguous last axes")
+        if not (-100 <= k_exp <= 100 and -100 <= v_exp <= 100 and int(k_exp) == k_exp and int(v_exp) == v_exp):
+            raise ValueError(f"exponents {k_exp}, {v_exp} are not integers in [-100, 100]")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_exp, self.v_exp, self.shape = int(k_exp), int(v_exp), (B, H, S, 2 * half)
         self._c = ba_kv4(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-                         *k_codes.stride()[:3], *k_scales.stride()[:3], self.k_exp, self.v_exp)
+                         cs[0], cs[1], cs[2], ss[0], ss[1], ss[2], self.k_exp, self.v_exp)
 
     @classmethod
     def empty(cls, B, H, S, d, *, device="cuda", k_exp=0, v_exp=0):

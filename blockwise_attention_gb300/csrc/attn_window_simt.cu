@@ -203,7 +203,8 @@ template <int D, typename T>
 int launch_t(const AttnArgs &a, long long blocks, cudaStream_t s) {
     constexpr size_t smem = window_simt_smem<D>();
     auto kern = window_simt_kernel<D, T>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return BA_ERR_CUDA;
+    static std::atomic<unsigned long long> allowed{0};
+    if (!allow_smem(allowed, reinterpret_cast<const void *>(kern), (int)smem)) return BA_ERR_CUDA;
     // rows read four elements at a time where every row is aligned for it
     const long long step = 4;
     auto fits = [&](const void *p, long long sB, long long sH, long long sT) {

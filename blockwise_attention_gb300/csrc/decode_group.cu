@@ -907,7 +907,8 @@ int launch_mma(const DecodeGroupArgs &a, cudaStream_t s) {
     constexpr int merge = DG_WARPS * (8 * NH * D + 32) * 4;
     constexpr int smem = R::BYTES > merge ? R::BYTES : merge;
     static_assert(mma_places(D, KV4, NH) * (smem + 1024) <= 233472, "shared memory of an SM");
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BA_ERR_CUDA;
+    static std::atomic<unsigned long long> allowed{0};
+    if (!allow_smem(allowed, reinterpret_cast<const void *>(kern), smem)) return BA_ERR_CUDA;
     kern<<<a.n_ctas, DG_WARPS * 32, smem, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return BA_ERR_CUDA;
     return launch_join<R::UNIT>(a, s);

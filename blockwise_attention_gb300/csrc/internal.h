@@ -5,9 +5,24 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace ba {
+
+// The dynamic shared memory that a kernel may use, set once for each device (`done`: a
+// bit for each, kept by the caller beside the kernel; a second setting by another thread
+// does no harm).
+inline bool allow_smem(std::atomic<unsigned long long> &done, const void *kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
 
 // Arguments of one attention launch (block or ring geometry).
 struct AttnArgs {

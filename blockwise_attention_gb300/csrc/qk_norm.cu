@@ -374,7 +374,8 @@ int launch_v(const QkNormArgs &a, const dim3 &grid, bool vec, cudaStream_t s) {
     constexpr size_t ring = (size_t)ring_rows<BWD> * (1 + (BWD ? Lane<T>::N * sizeof(G) / 16 : 0)) * QN_THREADS * 16;
     if (vec) {
         auto kern = qk_norm_kernel<T, G, LPR, BWD, true>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring) != cudaSuccess) return BA_ERR_CUDA;
+        static std::atomic<unsigned long long> allowed{0};
+        if (!allow_smem(allowed, reinterpret_cast<const void *>(kern), (int)ring)) return BA_ERR_CUDA;
         kern<<<grid, QN_THREADS, ring, s>>>(a);
     } else
         qk_norm_kernel<T, G, LPR, BWD, false><<<grid, QN_THREADS, 0, s>>>(a);
