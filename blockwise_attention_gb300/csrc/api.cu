@@ -1661,6 +1661,27 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok, in
 
 namespace {
 
+// base^(-2c/d) / (2 pi) times the position scale, as fractions of 2^64.  The powers take
+// longer than a launch, so each host thread keeps its last table.
+void turn_table(float base, float pos_scale, int d, unsigned long long (&turn)[64]) {
+    static thread_local struct {
+        float base, scale;
+        int d;
+        unsigned long long turn[64];
+    } last = {0.f, 0.f, 0, {}};
+    if (last.d != d || last.base != base || last.scale != pos_scale) {
+        for (int c = 0; c < d / 2; ++c) {
+            const double t = std::pow((double)base, -(double)(2 * c) / (double)d) *
+                             (pos_scale > 0.f ? (double)pos_scale : 1.0) / 6.283185307179586476925286766559;
+            last.turn[c] = (unsigned long long)((t - std::floor(t)) * 0x1p64);   // (whole turns do not matter: m is an integer)
+        }
+        last.base = base;
+        last.scale = pos_scale;
+        last.d = d;
+    }
+    std::memcpy(turn, last.turn, sizeof turn);
+}
+
 // Checks what the forward and the backward share and fills it in; BA_OK with
 // a.places = 0 when there is nothing to do.
 int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, const void *wk, int w_dtype, int B, int Hq,
@@ -1701,11 +1722,7 @@ int qk_norm_args(ba::QkNormArgs &a, ba_tensor q, ba_tensor k, const void *wq, co
     a.eps = eps;
     a.positions = positions;
     a.pos_ld = positions_ld;
-    for (int c = 0; c < d / 2; ++c) {
-        const double turn = std::pow((double)base, -(double)(2 * c) / (double)d) *
-                            (pos_scale > 0.f ? (double)pos_scale : 1.0) / 6.283185307179586476925286766559;
-        a.turn[c] = (unsigned long long)((turn - std::floor(turn)) * 0x1p64);   // (whole turns do not matter: m is an integer)
-    }
+    turn_table(base, pos_scale, d, a.turn);
     const bool own = positions && positions_ld > 0;   // each sequence has its own positions
     a.places = own ? (long long)B * T : T;
     a.nb = own ? 1 : B;
@@ -1836,6 +1853,12 @@ int check_window(int B, int Hq, int Hkv, int Lq, int Lk, int dtype, int64_t q_of
     return BA_OK;
 }
 
+// Rows that the tensor-core kernels can read by TMA; axes that are broadcast (stride 0) are
+// left to the CUDA-core kernels.
+bool window_tma_ok(const ba_tensor &t, int B, int H) {
+    return tma_ok(t, B, H) && t.sT > 0 && (H <= 1 || t.sH > 0) && (B <= 1 || t.sB > 0);
+}
+
 int window_heads_per_group(int B, int Hq, int Hkv, long long keys, int d, int dtype) {
     return heads_per_group(B, Hkv, keys, d, dtype) * (Hq / Hkv);
 }
@@ -1905,7 +1928,8 @@ int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hk
     a.rows = Lq;
     a.err = g_err_ptr[dev];
     a.wait_limit_ns = kWaitLimitNs;
-    if (!tc_supported(dtype, d) || Lk == 0 || !tma_ok(q, B, Hq) || !tma_ok(k, B, Hkv) || !tma_ok(v, B, Hkv))
+    if (!tc_supported(dtype, d) || Lk == 0 || !window_tma_ok(q, B, Hq) || !window_tma_ok(k, B, Hkv) ||
+        !window_tma_ok(v, B, Hkv))
         return launch_window_simt(a, stream);
     if ((rc = get_encoder())) return rc;
     // With no more items than SMs every CTA takes one: dealt round-robin, without the
@@ -2000,8 +2024,8 @@ int attn_window_bwd(ba_tensor q, ba_tensor k, ba_tensor v, ba_tensor out, ba_ten
     a.err = g_err_ptr[dev];
     a.wait_limit_ns = kWaitLimitNs;
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };   // 16-byte stores
-    const bool tc = ba::bwd_tc_supported(dtype, d) && tma_ok(q, B, Hq) && tma_ok(k, B, Hkv) && tma_ok(v, B, Hkv) &&
-                    tma_ok(dout, B, Hq) && al16(dq) && al16(dk) && al16(dv);
+    const bool tc = ba::bwd_tc_supported(dtype, d) && window_tma_ok(q, B, Hq) && window_tma_ok(k, B, Hkv) &&
+                    window_tma_ok(v, B, Hkv) && window_tma_ok(dout, B, Hq) && al16(dq) && al16(dk) && al16(dv);
     const SinkParts p = sink_parts(w, Lq, tc ? TILE : 64);
     a.n_sink_tiles = p.tiles;
     a.n_sink_parts = p.parts;

@@ -54,7 +54,7 @@ namespace {
 // ST: the layout has the output staging region (instantiations that store
 // full tiles by TMA); without it the shared-memory carve-out stays smaller,
 // which leaves more L1 for the long-walk kernel's spill slots.
-template <int D, int ST>
+template <int D, bool ST>
 struct Cfg {
     static constexpr int NBOX = D / 64;            // 64-column boxes per tile
     static constexpr int BOX_BYTES = TILE * 128;   // 128 rows x 128 bytes

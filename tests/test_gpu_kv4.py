@@ -223,6 +223,39 @@ def test_prompt_then_tokens_as_served():
         ref.check_forward(*got, nq, ck, cv, seen, label=f"token {t}", p_step=P_STEP)
 
 
+def test_empty_caches_chunks_and_sequences():
+    cache = ba.KV4Cache.empty(2, 2, 0, 64)
+    x = rand((2, 2, 3, 64), torch.bfloat16, 40)
+    ba.kv4_append(cache, x, x)
+    out, lse = ba.attn_decode_kv4_fwd(x[:, :, :1], cache)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    cache = filled(2, 2, 9, 64, 41)
+    before = [t.clone() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    ba.kv4_append(cache, x[:, :, :0], x[:, :, :0])
+    ba.kv4_append(cache, x, x, counts=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    ba.kv4_append(cache, x, x, start=torch.tensor([-3, 9], dtype=torch.int32, device="cuda"))
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)))
+    assert ba.kv4_read(cache, 0)[0].shape == (2, 2, 0, 64)
+    many = filled(300, 1, 50, 64, 42)
+    check(rand((300, 2, 1, 64), torch.bfloat16, 43), many, [(b * 7) % 51 for b in range(300)], 0, 0, "many sequences")
+
+
+def test_long_chunks_with_any_strides():
+    """Chunks of many rows into a cache stored (B, S, H, ..), starts that are not multiples of anything."""
+    B, H, T, S, d = 2, 3, 500, 777, 128
+    st = [torch.zeros((B, S, H, n), dtype=torch.uint8, device="cuda").permute(0, 2, 1, 3) for n in (64, 8, 64, 8)]
+    cache = ba.KV4Cache(*st)
+    k, v = (rand((B, T, H, d), torch.float32, 44 + i).permute(0, 2, 1, 3) for i in range(2))
+    start = torch.tensor([277, 11], dtype=torch.int32, device="cuda")
+    ba.kv4_append(cache, k, v, start=start)
+    got = ba.kv4_read(cache, S, dtype=torch.float32)
+    for x, y in zip((k, v), got):
+        for b in range(B):
+            n = int(start[b])
+            assert torch.equal(y[b, :, n:n + T].double(), quantise(x[b], 0)[2])
+            assert (y[b, :, :n] == 0).all() and (y[b, :, n + T:] == 0).all()
+
+
 def test_binding_refusals():
     cache = ba.KV4Cache.empty(2, 2, 40, 64)
     x = rand((2, 2, 3, 64), torch.bfloat16, 30)

@@ -87,6 +87,20 @@ def test_strided_inputs_and_any_alignment(dt, d):
     both(*odd, window=100, sinks=2, label="odd strides")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_broadcast_inputs_and_empty_sides(dt):
+    """Keys shared by the batch (stride 0), a cotangent of one value, and axes of length zero."""
+    q, k, v, g = inputs(3, 4, 2, 150, 150, 64, dt, 45)
+    both(q, k[:1].expand(3, -1, -1, -1), v[:1].expand(3, -1, -1, -1), g, window=60, sinks=2, label="batch shared")
+    both(q, k, v, g[:1, :1, :1, :1].expand_as(g).contiguous(), window=60, sinks=2, label="one value")
+    both(q, k[:, :1].expand(3, 2, 150, 64), v, g, window=60, sinks=2, label="head shared")
+    for q0, k0 in ((q[:0], k[:0]), (q[:, :, :0], k), (q, k[:, :, :0])):
+        out, lse = ba.attn_window_fwd(q0, k0, k0, window=9)
+        dq, dk, dv = ba.attn_window_bwd(q0, k0, k0, out, out, lse, window=9)
+        assert out.shape == q0.shape and (out == 0).all() and (lse == -math.inf).all()
+        assert dq.shape == q0.shape and dk.shape == k0.shape and (dq == 0).all() and (dk == 0).all() and (dv == 0).all()
+
+
 @pytest.mark.parametrize("dt,d", [("bf16", 64), ("f32", 64)])
 def test_sink_tiles_split_over_long_sequences(dt, d):
     """A window far shorter than the sequence: the sinks' gradients come from many chunks."""

@@ -49,6 +49,20 @@ def test_cache_sizes_and_splits(dt, d, S, window):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_empty_caches_batches_and_many_sequences(dt):
+    q = rand((2, 4, 1, 64), DT[dt], 30)
+    empty = rand((2, 2, 0, 64), DT[dt], 31)
+    out, lse = ba.attn_window_decode_fwd(q, empty, empty, window=5, sinks=1)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    out, lse = ba.attn_window_decode_fwd(q[:0], empty[:0], empty[:0], window=5)
+    assert out.shape == (0, 4, 1, 64)
+    B, S = 300, 90   # more sequences than the scan takes at a time, most of them short or empty
+    lengths = [(b * 37) % 91 if b % 3 else 0 for b in range(B)]
+    k, v = rand((1, 2, S, 64), DT[dt], 32).expand(B, -1, -1, -1), rand((B, 2, S, 64), DT[dt], 33)
+    check(rand((B, 4, 1, 64), DT[dt], 34), k, v, lengths, 40, 3, "many")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_strided_cache_large_scores_and_out_types(dt):
     """A cache stored (B, S, H, d); scores up to about a hundred (the running maximum moves often)."""
     B, Hq, Hkv, S, d = 3, 8, 2, 1500, 64
