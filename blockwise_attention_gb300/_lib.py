@@ -10,8 +10,10 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 import torch
@@ -21,6 +23,7 @@ _ROOT = os.path.dirname(_PKG)
 _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_BUILD, "libblockattn.so")
+FASTCALL_PATH = os.path.join(_BUILD, "_fastcall.so")
 _SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu",
             "decode_group.cu", "kv4.cu", "qk_norm.cu", "attn_window_simt.cu"]
 _HEADERS = ["common.cuh", "internal.h", "epilogue.cuh", "tc_ptx.cuh"]
@@ -36,6 +39,7 @@ MODES = {"stepwise": 0, "fused": 1}
 BA_TILE_EMPTY, BA_TILE_FULL, BA_TILE_PARTIAL = 0, 1, 2
 
 _lib = None
+_fast = None   # the module of csrc/fastcall.c, where the interpreter's headers are installed
 
 
 class BlockAttnError(RuntimeError):
@@ -61,8 +65,27 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_fastcall(force):
+    """Compile csrc/fastcall.c with the host compiler, where Python.h is installed."""
+    src, header = os.path.join(_CSRC, "fastcall.c"), os.path.join(_ROOT, "include", "blockattn.h")
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    if not force and os.path.exists(FASTCALL_PATH) and \
+            os.path.getmtime(FASTCALL_PATH) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    os.makedirs(_BUILD, exist_ok=True)
+    tmp = FASTCALL_PATH + f".tmp{os.getpid()}"
+    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", os.path.join(_ROOT, "include"), "-I",
+                        include, src, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{src} did not compile:\n{r.stderr}")
+    os.replace(tmp, FASTCALL_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources for sm_103a (in parallel) and link the shared library."""
+    _build_fastcall(force)
     if not force and not _stale():
         return LIB_PATH
     os.makedirs(_BUILD, exist_ok=True)
@@ -201,7 +224,19 @@ def load(path: str | None = None):
     lib.qk_norm_rope_bwd.argtypes = [T, T, vp, vp, i, T, T, i, i, i, i, i, i, i, f, vp, i64, f, f, vp, vp, vp, vp, vp, sz,
                                      vp]
     _lib = lib
+    if os.path.exists(FASTCALL_PATH):
+        _load_fastcall(lib)
     return lib
+
+
+def _load_fastcall(lib):
+    global _fast
+    spec = importlib.util.spec_from_file_location("_fastcall", FASTCALL_PATH)
+    fast = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fast)
+    fast.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED}, torch.empty, torch.bfloat16,
+              torch.float32, torch.uint8, torch.int32, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _fast = fast
 
 
 def _check(fn, rc):
@@ -503,8 +538,10 @@ def ulysses_attn_fwd(q_tok, k_tok, v_tok, *, key_padding_mask=None, attn_mask=No
 
 
 # Helpers of the entry points below.  A single-token call is over on the GPU in a few
-# microseconds, so what the binding does per call is kept short: one stride() per tensor,
-# devices and streams as integers, sizes of workspaces remembered.
+# microseconds, so a call that leaves its outputs, workspace and stream to the binding is
+# marshalled in C (csrc/fastcall.c), which answers None to whatever is out of the ordinary.
+# That, and everything that is to be refused, goes on here: one stride() per tensor, devices
+# and streams as integers, sizes of workspaces remembered.
 
 _DTYPES = {torch.float32: BA_F32, torch.bfloat16: BA_BF16}
 
@@ -619,6 +656,10 @@ def attn_window_fwd(q, k, v, *, window, sinks=0, q_off=0, key_padding_mask=None,
     q (B, Hq, Lq, d) at positions q_off + i against k, v (B, Hkv, Lk, d) at positions
     0 .. Lk - 1, Hkv dividing Hq; see include/blockattn.h.  Returns (out, lse)."""
     lib = load()
+    if _fast is not None and out is out_dtype is lse is workspace is stream is None:
+        r = _fast.attn_window_fwd(q, k, v, window, sinks, q_off, key_padding_mask, scale)
+        if r is not None:
+            return r
     B, Hq, Lq, d, Hkv, Lk = _kv_heads(q, k, v)
     window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
     dt = _code(q.dtype)
@@ -639,6 +680,10 @@ def attn_window_bwd(q, k, v, out, dout, lse, *, window, sinks=0, q_off=0, key_pa
     """Gradients (dq, dk, dv) of attn_window_fwd from its out and lse; of q's dtype
     unless grad_dtype (or the given buffers) say float32; see include/blockattn.h."""
     lib = load()
+    if _fast is not None and dq is dk is dv is grad_dtype is workspace is stream is None:
+        r = _fast.attn_window_bwd(q, k, v, out, dout, lse, window, sinks, q_off, key_padding_mask, scale)
+        if r is not None:
+            return r
     B, Hq, Lq, d, Hkv, Lk = _kv_heads(q, k, v)
     window, sinks, q_off = _c_int("window", window, 1), _c_int("sinks", sinks, 0), _c_int("q_off", q_off, 0)
     dt = _code(q.dtype)
@@ -705,6 +750,10 @@ def attn_window_decode_fwd(q, k_cache, v_cache, *, window, sinks=0, lengths=None
     against the caches (B, Hkv, S, d), Hkv dividing Hq; lengths: int32 (B) or None (S).
     Returns (out, lse)."""
     lib = load()
+    if _fast is not None and out is out_dtype is lse is workspace is stream is None:
+        r = _fast.attn_window_decode_fwd(q, k_cache, v_cache, window, sinks, lengths, scale)
+        if r is not None:
+            return r
     B, Hq, one, d, Hkv, S = _kv_heads(q, k_cache, v_cache)
     if one != 1:
         raise ValueError("decode takes one query per (b, h): q of shape (B, Hq, 1, d)")
@@ -726,7 +775,7 @@ class KV4Cache:
     """A KV cache held in 4 bits: codes (B, H, S, d / 2) and scales (B, H, S, d / 16), uint8,
     of K and of V, with the tensors' powers of two; see include/blockattn.h (ba_kv4)."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_exp", "v_exp", "shape", "_c")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_exp", "v_exp", "shape", "dev", "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_exp=0, v_exp=0):
         dev = k_codes.get_device()
@@ -744,7 +793,7 @@ class KV4Cache:
         if not (-100 <= k_exp <= 100 and -100 <= v_exp <= 100 and int(k_exp) == k_exp and int(v_exp) == v_exp):
             raise ValueError(f"exponents {k_exp}, {v_exp} are not integers in [-100, 100]")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_exp, self.v_exp, self.shape = int(k_exp), int(v_exp), (B, H, S, 2 * half)
+        self.k_exp, self.v_exp, self.shape, self.dev = int(k_exp), int(v_exp), (B, H, S, 2 * half), dev
         self._c = ba_kv4(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                          cs[0], cs[1], cs[2], ss[0], ss[1], ss[2], self.k_exp, self.v_exp)
 
@@ -760,6 +809,10 @@ def kv4_append(cache, k, v, *, start=None, counts=None, stream=None):
     """Quantise k, v (B, H, T, d) into the slots start[b] + t of a KV4Cache (t < counts[b]);
     start, counts: int32 (B) CUDA tensors or None (0, T).  Slots outside the cache are dropped."""
     lib = load()
+    if _fast is not None and stream is None:
+        r = _fast.kv4_append(cache, k, v, start, counts)
+        if r is not None:
+            return r
     B, H, S, d = cache.shape
     shape = k.shape
     if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype or shape[0] != B or shape[1] != H or shape[3] != d:
@@ -775,6 +828,10 @@ def kv4_append(cache, k, v, *, start=None, counts=None, stream=None):
 def kv4_read(cache, T, *, first=0, dtype=torch.bfloat16, out_k=None, out_v=None, stream=None):
     """The values of slots first .. first + T - 1 of a KV4Cache: (k, v), each (B, H, T, d)."""
     lib = load()
+    if _fast is not None and out_k is out_v is stream is None:
+        r = _fast.kv4_read(cache, T, first, dtype)
+        if r is not None:
+            return r
     B, H, S, d = cache.shape
     T, first, dt = _c_int("T", T, 0), _c_int("first", first, 0), _code(dtype)
     codes = cache.k_codes
@@ -791,6 +848,10 @@ def attn_decode_kv4_fwd(q, cache, *, lengths=None, window=0, sinks=0, scale=None
     """Single-token attention of q (B, Hq, 1, d) bf16 over a KV4Cache of (B, Hkv, S, d), over
     every key (window = 0) or a window with sinks; see include/blockattn.h.  Returns (out, lse)."""
     lib = load()
+    if _fast is not None and out is out_dtype is lse is workspace is stream is None:
+        r = _fast.attn_decode_kv4_fwd(q, cache, lengths, window, sinks, scale)
+        if r is not None:
+            return r
     B, Hkv, S, d = cache.shape
     shape = tuple(q.shape)
     if len(shape) != 4 or shape[0] != B or shape[2] != 1 or shape[3] != d or Hkv == 0 or shape[1] % Hkv:
@@ -859,6 +920,10 @@ def qk_norm_rope_fwd(q, k, wq, wk, *, eps=1e-6, positions=None, base=10000.0, po
     wq, wk (d); positions: int32 (T,) or (B, T), None: 0 .. T - 1; see include/blockattn.h.
     Returns (yq, yk), contiguous."""
     lib = load()
+    if _fast is not None and out_q is out_k is stream is None:
+        r = _fast.qk_norm_rope_fwd(q, k, wq, wk, eps, positions, base, pos_scale)
+        if r is not None:
+            return r
     tq, tk = _view("q", q), _view("k", k)
     sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
     dev = _device(q, k=k, wq=wq, wk=wk, positions=positions)
@@ -874,6 +939,10 @@ def qk_norm_rope_bwd(q, k, wq, wk, dyq, dyk, *, eps=1e-6, positions=None, base=1
     """Gradients (dq, dk, dwq, dwk) of qk_norm_rope_fwd for dyq, dyk (of q's dtype or
     float32): dq, dk of q's dtype, dwq, dwk float32."""
     lib = load()
+    if _fast is not None and dq is dk is workspace is stream is None:
+        r = _fast.qk_norm_rope_bwd(q, k, wq, wk, eps, positions, base, pos_scale, dyq, dyk)
+        if r is not None:
+            return r
     tensors = _view("q", q), _view("k", k), _view("dyq", dyq), _view("dyk", dyk)
     sizes, wdt, pos, ld = _norm_inputs(q, k, wq, wk, positions)
     if dyq.shape != q.shape or dyk.shape != k.shape:
