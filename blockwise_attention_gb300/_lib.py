@@ -23,7 +23,7 @@ _ROOT = os.path.dirname(_PKG)
 _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_BUILD, "libblockattn.so")
-FASTCALL_PATH = os.path.join(_BUILD, "_fastcall.so")
+FASTCALL_PATH = os.path.join(_BUILD, f"_fastcall_torch{torch.__version__}.so")   # (its ABI is that of one version)
 _SOURCES = ["api.cu", "attn_simt.cu", "attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "ulysses.cu", "decode.cu",
             "decode_group.cu", "kv4.cu", "qk_norm.cu", "attn_window_simt.cu"]
 _HEADERS = ["common.cuh", "internal.h", "epilogue.cuh", "tc_ptx.cuh"]
@@ -39,7 +39,7 @@ MODES = {"stepwise": 0, "fused": 1}
 BA_TILE_EMPTY, BA_TILE_FULL, BA_TILE_PARTIAL = 0, 1, 2
 
 _lib = None
-_fast = None   # the module of csrc/fastcall.c, where the interpreter's headers are installed
+_fast = None   # the module of csrc/fastcall.cpp, where the interpreter's headers are installed
 
 
 class BlockAttnError(RuntimeError):
@@ -66,28 +66,41 @@ def _stale() -> bool:
 
 
 def _build_fastcall(force):
-    """Compile csrc/fastcall.c with the host compiler, where Python.h is installed."""
-    src, header = os.path.join(_CSRC, "fastcall.c"), os.path.join(_ROOT, "include", "blockattn.h")
-    include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
+    """Compile csrc/fastcall.cpp against torch, where the interpreter's headers are installed."""
+    src, header = os.path.join(_CSRC, "fastcall.cpp"), os.path.join(_ROOT, "include", "blockattn.h")
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
         return
     if not force and os.path.exists(FASTCALL_PATH) and \
             os.path.getmtime(FASTCALL_PATH) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return
     os.makedirs(_BUILD, exist_ok=True)
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [os.path.join(_ROOT, "include"), python, os.path.join(torch_dir, "include"), cuda]
+    libs = os.path.join(torch_dir, "lib")
     tmp = FASTCALL_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", os.path.join(_ROOT, "include"), "-I",
-                        include, src, "-o", tmp], capture_output=True, text=True)
+    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in includes), src, "-o", tmp,
+           f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{src} did not compile:\n{r.stderr}")
     os.replace(tmp, FASTCALL_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the CUDA sources for sm_103a (in parallel) and link the shared library."""
-    _build_fastcall(force)
+    """Compile the CUDA sources for sm_103a and the call marshalling (in parallel) and link the shared library."""
+    with ThreadPoolExecutor(1) as ex:
+        fastcall = ex.submit(_build_fastcall, force)
+        _build_library(force, verbose)
+        fastcall.result()
+    return LIB_PATH
+
+
+def _build_library(force, verbose):
     if not force and not _stale():
-        return LIB_PATH
+        return
     os.makedirs(_BUILD, exist_ok=True)
     nvcc = _nvcc()
     common = [nvcc, *ARCH_FLAGS, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -110,7 +123,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 class ba_tensor(ctypes.Structure):
@@ -234,8 +246,7 @@ def _load_fastcall(lib):
     spec = importlib.util.spec_from_file_location("_fastcall", FASTCALL_PATH)
     fast = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fast)
-    fast.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED}, torch.empty, torch.bfloat16,
-              torch.float32, torch.uint8, torch.int32, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    fast.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in EXPORTED})
     _fast = fast
 
 
@@ -539,7 +550,7 @@ def ulysses_attn_fwd(q_tok, k_tok, v_tok, *, key_padding_mask=None, attn_mask=No
 
 # Helpers of the entry points below.  A single-token call is over on the GPU in a few
 # microseconds, so a call that leaves its outputs, workspace and stream to the binding is
-# marshalled in C (csrc/fastcall.c), which answers None to whatever is out of the ordinary.
+# marshalled in C++ (csrc/fastcall.cpp), which answers None to whatever is out of the ordinary.
 # That, and everything that is to be refused, goes on here: one stride() per tensor, devices
 # and streams as integers, sizes of workspaces remembered.
 

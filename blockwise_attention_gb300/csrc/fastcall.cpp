@@ -1,110 +1,107 @@
 /* The common calls of the windowed, grouped-head, 4-bit and norm entry points, marshalled
- * in C: outputs and workspace from torch's allocator, the current stream, no buffer of the
- * caller's.  A single-token call is over on the GPU in a few microseconds, and the same
- * steps in Python took twenty.
+ * in C++: outputs and workspace from torch's allocator, the current stream, no buffer of the
+ * caller's.  A single-token call is over on the GPU in a few microseconds; the same steps in
+ * Python take 22 us of host time for the decode of one sequence, here 8.
  *
  * Every function takes the positional arguments that the Python function of its name
  * passes on, checks all that that function checks, and returns its result, or None when
  * anything is out of the ordinary: the Python function then goes through its own checks
  * and raises what is to be raised.  No computation, and nothing kept between calls but
- * the interned names and the library's addresses. */
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
+ * the library's addresses. */
+#include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/Dtype.h>
 
-#include <string.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <cstring>
 
 #include "blockattn.h"
 
-static struct {
-    __typeof__(&attn_window_fwd) attn_window_fwd;
-    __typeof__(&attn_window_fwd_workspace_size) attn_window_fwd_workspace_size;
-    __typeof__(&attn_window_bwd) attn_window_bwd;
-    __typeof__(&attn_window_bwd_workspace_size) attn_window_bwd_workspace_size;
-    __typeof__(&attn_window_decode_fwd) attn_window_decode_fwd;
-    __typeof__(&attn_window_decode_workspace_size) attn_window_decode_workspace_size;
-    __typeof__(&kv4_append) kv4_append;
-    __typeof__(&kv4_read) kv4_read;
-    __typeof__(&attn_decode_kv4_fwd) attn_decode_kv4_fwd;
-    __typeof__(&attn_decode_kv4_workspace_size) attn_decode_kv4_workspace_size;
-    __typeof__(&qk_norm_rope_fwd) qk_norm_rope_fwd;
-    __typeof__(&qk_norm_rope_bwd) qk_norm_rope_bwd;
-    __typeof__(&qk_norm_rope_bwd_workspace_size) qk_norm_rope_bwd_workspace_size;
+namespace {
+
+struct {
+    decltype(&::attn_window_fwd) attn_window_fwd;
+    decltype(&::attn_window_fwd_workspace_size) attn_window_fwd_workspace_size;
+    decltype(&::attn_window_bwd) attn_window_bwd;
+    decltype(&::attn_window_bwd_workspace_size) attn_window_bwd_workspace_size;
+    decltype(&::attn_window_decode_fwd) attn_window_decode_fwd;
+    decltype(&::attn_window_decode_workspace_size) attn_window_decode_workspace_size;
+    decltype(&::kv4_append) kv4_append;
+    decltype(&::kv4_read) kv4_read;
+    decltype(&::attn_decode_kv4_fwd) attn_decode_kv4_fwd;
+    decltype(&::attn_decode_kv4_workspace_size) attn_decode_kv4_workspace_size;
+    decltype(&::qk_norm_rope_fwd) qk_norm_rope_fwd;
+    decltype(&::qk_norm_rope_bwd) qk_norm_rope_bwd;
+    decltype(&::qk_norm_rope_bwd_workspace_size) qk_norm_rope_bwd_workspace_size;
 } L;
 
-static PyObject *t_empty, *t_bf16, *t_f32, *t_u8, *t_i32, *t_device, *t_stream;   /* torch's */
-static PyObject *s_shape, *s_dtype, *s_stride, *s_ptr, *s_dev, *s_c, *kw_empty;
+PyObject *s_shape, *s_dev, *s_c;   // attributes of a KV4Cache
 
-/* A tensor of up to four axes.  code: BA_F32, BA_BF16, 2 for uint8, 3 for int32. */
-typedef struct {
+// A plain tensor of up to four axes.  code: BA_F32, BA_BF16, 2 for uint8, 3 for int32.
+struct Ten {
     int n, code;
     long dev;
     long long size[4], step[4];
     void *ptr;
-} Ten;
+};
 
-static int ints(PyObject *t, long long *to) {
-    if (!t || !PyTuple_Check(t) || PyTuple_GET_SIZE(t) > 4) return -1;
-    const int n = (int)PyTuple_GET_SIZE(t);
-    for (int i = 0; i < n; ++i) {
-        to[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
-        if (to[i] == -1 && PyErr_Occurred()) return -1;
+bool read_tensor(PyObject *x, Ten *t) {
+    if (!THPVariable_CheckExact(x)) return false;
+    const at::Tensor &v = THPVariable_Unpack(x);
+    if (!v.is_cuda() || v.layout() != at::kStrided || v.is_neg() || v.dim() > 4) return false;
+    switch (v.scalar_type()) {
+        case at::kFloat: t->code = BA_F32; break;
+        case at::kBFloat16: t->code = BA_BF16; break;
+        case at::kByte: t->code = 2; break;
+        case at::kInt: t->code = 3; break;
+        default: return false;
     }
-    return n;
+    t->n = (int)v.dim();
+    const auto size = v.sizes(), step = v.strides();
+    for (int i = 0; i < t->n; ++i) {
+        t->size[i] = size[i];
+        t->step[i] = step[i];
+    }
+    t->dev = v.get_device();
+    t->ptr = v.data_ptr();
+    return true;
 }
 
-static int read_tensor(PyObject *x, Ten *t) {
-    PyObject *o = PyObject_GetAttr(x, s_shape);
-    t->n = ints(o, t->size);
-    Py_XDECREF(o);
-    if (t->n < 0) return 0;
-    o = PyObject_CallMethodNoArgs(x, s_stride);
-    const int n = ints(o, t->step);
-    Py_XDECREF(o);
-    if (n != t->n) return 0;
-    if (!(o = PyObject_GetAttr(x, s_dtype))) return 0;
-    t->code = o == t_bf16 ? BA_BF16 : o == t_f32 ? BA_F32 : o == t_u8 ? 2 : o == t_i32 ? 3 : -1;
-    Py_DECREF(o);
-    if (t->code < 0 || !(o = PyObject_CallMethodNoArgs(x, s_dev))) return 0;
-    t->dev = PyLong_AsLong(o);
-    Py_DECREF(o);
-    if (t->dev < 0 || !(o = PyObject_CallMethodNoArgs(x, s_ptr))) return 0;
-    t->ptr = PyLong_AsVoidPtr(o);
-    Py_DECREF(o);
-    return !PyErr_Occurred();
-}
-
-static ba_tensor view(const Ten *t) {
+ba_tensor view(const Ten *t) {
     const ba_tensor v = {t->ptr, t->step[0], t->step[1], t->step[2]};
     return v;
 }
 
-static int heads(const Ten *t) { return t->n == 4 && t->code <= BA_BF16 && (t->step[3] == 1 || t->size[3] <= 1); }
-static int fits(const Ten *t) {   /* sizes that the entry points take as int */
+int heads(const Ten *t) { return t->n == 4 && t->code <= BA_BF16 && (t->step[3] == 1 || t->size[3] <= 1); }
+int fits(const Ten *t) {   /* sizes that the entry points take as int */
     for (int i = 0; i < t->n; ++i)
         if (t->size[i] > 0x7fffffffLL) return 0;
     return 1;
 }
-static int same(const Ten *a, const Ten *b) {   /* shape, dtype and device */
+int same(const Ten *a, const Ten *b) {   /* shape, dtype and device */
     if (a->n != b->n || a->code != b->code || a->dev != b->dev) return 0;
     for (int i = 0; i < a->n; ++i)
         if (a->size[i] != b->size[i]) return 0;
     return 1;
 }
 /* k, v (B, Hkv, L, d) beside q (B, Hq, .., d). */
-static int grouped(const Ten *q, const Ten *k, const Ten *v) {
+int grouped(const Ten *q, const Ten *k, const Ten *v) {
     return heads(q) && heads(k) && heads(v) && same(k, v) && k->code == q->code && k->dev == q->dev &&
            k->size[0] == q->size[0] && k->size[3] == q->size[3] && k->size[1] > 0 && q->size[1] % k->size[1] == 0 && fits(q) &&
            fits(k);
 }
 
-static int whole(PyObject *o, long long lo, int *to) {
+int whole(PyObject *o, long long lo, int *to) {
     if (!PyLong_CheckExact(o)) return 0;
     const long long v = PyLong_AsLongLong(o);
     if ((v == -1 && PyErr_Occurred()) || v < lo || v > 0x7fffffffLL) return 0;
     *to = (int)v;
     return 1;
 }
-static int real(PyObject *o, float *to) {   /* None: 0 */
+int real(PyObject *o, float *to) {   /* None: 0 */
     if (o == Py_None) {
         *to = 0.f;
         return 1;
@@ -115,9 +112,9 @@ static int real(PyObject *o, float *to) {   /* None: 0 */
 }
 
 /* An int32 entry for each of B sequences, or None. */
-static int per_sequence(PyObject *o, long long B, long dev, const int32_t **to) {
+int per_sequence(PyObject *o, long long B, long dev, const int32_t **to) {
     Ten t;
-    *to = NULL;
+    *to = nullptr;
     if (o == Py_None) return 1;
     if (!read_tensor(o, &t) || t.code != 3 || t.n != 1 || t.size[0] != B || (B > 1 && t.step[0] != 1) || t.dev != dev) return 0;
     *to = (const int32_t *)t.ptr;
@@ -125,9 +122,9 @@ static int per_sequence(PyObject *o, long long B, long dev, const int32_t **to) 
 }
 
 /* A key-padding mask of at least B rows and `keys` columns, or None. */
-static int padding(PyObject *o, long long B, long long keys, long dev, const uint8_t **to, int64_t *ld) {
+int padding(PyObject *o, long long B, long long keys, long dev, const uint8_t **to, int64_t *ld) {
     Ten t;
-    *to = NULL;
+    *to = nullptr;
     *ld = 0;
     if (o == Py_None) return 1;
     if (!read_tensor(o, &t) || t.code != 2 || t.n != 2 || t.dev != dev || t.size[0] < B || t.size[1] < keys || t.step[1] != 1 ||
@@ -139,73 +136,48 @@ static int padding(PyObject *o, long long B, long long keys, long dev, const uin
 }
 
 /* dev is the current device: its current stream. */
-static int stream_of(long dev, ba_stream_t *to) {
-    PyObject *o = PyObject_CallNoArgs(t_device);
-    if (!o) return 0;
-    const long cur = PyLong_AsLong(o);
-    Py_DECREF(o);
-    if (cur != dev) return 0;
-    PyObject *d = PyLong_FromLong(dev);
-    o = d ? PyObject_CallOneArg(t_stream, d) : NULL;
-    Py_XDECREF(d);
-    if (!o) return 0;
-    *to = (ba_stream_t)PyLong_AsVoidPtr(o);
-    Py_DECREF(o);
-    return !PyErr_Occurred();
+int stream_of(long dev, ba_stream_t *to) {
+    if (c10::cuda::current_device() != dev) return 0;
+    *to = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+    return 1;
 }
 
-/* torch.empty(size, dtype=, device=) and its pointer. */
-static PyObject *empty(int n, const long long *size, PyObject *dtype, long dev, void **ptr) {
-    PyObject *shape = PyTuple_New(n), *d = PyLong_FromLong(dev), *r = NULL;
-    if (shape && d) {
-        for (int i = 0; i < n; ++i) PyTuple_SET_ITEM(shape, i, PyLong_FromLongLong(size[i]));
-        PyObject *args[3] = {shape, dtype, d};
-        r = PyObject_Vectorcall(t_empty, args, 1, kw_empty);
-    }
-    Py_XDECREF(shape);
-    Py_XDECREF(d);
-    if (!r) return NULL;
-    PyObject *p = PyObject_CallMethodNoArgs(r, s_ptr);
-    if (!p) {
-        Py_DECREF(r);
-        return NULL;
-    }
-    *ptr = PyLong_AsVoidPtr(p);
-    Py_DECREF(p);
-    return r;
+/* A new contiguous tensor and its pointer. */
+at::Tensor empty(int n, const long long *size, int code, long dev, void **ptr) {
+    int64_t z[4];
+    for (int i = 0; i < n; ++i) z[i] = size[i];
+    const at::ScalarType type = code == BA_BF16 ? at::kBFloat16 : code == BA_F32 ? at::kFloat : at::kByte;
+    at::Tensor t = at::detail::empty_cuda(at::IntArrayRef(z, n), type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+    *ptr = t.data_ptr();
+    return t;
 }
-static int scratch(size_t need, long dev, PyObject **t, void **ptr) {
+at::Tensor scratch(size_t need, long dev, void **ptr) {
     const long long n = (long long)need;
-    *t = NULL;
-    *ptr = NULL;
-    return need == 0 || (*t = empty(1, &n, t_u8, dev, ptr)) != NULL;
+    *ptr = nullptr;
+    return need ? empty(1, &n, 2, dev, ptr) : at::Tensor();
 }
-static PyObject *type_of(int code) { return code == BA_BF16 ? t_bf16 : t_f32; }
 
+PyObject *other_way(void) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
 /* n results as a tuple when the call went well; otherwise None (the Python function calls
  * again and raises). */
-static PyObject *results(int rc, int n, PyObject **r, PyObject *ws) {
-    int ok = rc == BA_OK;
-    for (int i = 0; i < n; ++i) ok = ok && r[i];
-    PyObject *t = ok ? PyTuple_New(n) : NULL;
-    for (int i = 0; i < n; ++i) {
-        if (t)
-            PyTuple_SET_ITEM(t, i, r[i]);
-        else
-            Py_XDECREF(r[i]);
+PyObject *results(int rc, int n, at::Tensor *r) {
+    PyObject *t = rc == BA_OK ? PyTuple_New(n) : nullptr;
+    for (int i = 0; t && i < n; ++i) {
+        PyObject *x = THPVariable_Wrap(std::move(r[i]));
+        if (!x) {
+            Py_CLEAR(t);
+            break;
+        }
+        PyTuple_SET_ITEM(t, i, x);
     }
-    Py_XDECREF(ws);
-    if (t) return t;
-    PyErr_Clear();
-    Py_RETURN_NONE;
-}
-static PyObject *other_way(void) {
-    PyErr_Clear();
-    Py_RETURN_NONE;
+    return t ? t : other_way();
 }
 
 /* (q, k, v, window, sinks, q_off, key_padding_mask, scale) -> (out, lse) */
-static PyObject *window_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *window_fwd(PyObject *const *a, Py_ssize_t na) {
     Ten q, k, v;
     int window, sinks, off;
     const uint8_t *kpm;
@@ -218,22 +190,23 @@ static PyObject *window_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
         return other_way();
     const int B = (int)q.size[0], Hq = (int)q.size[1], Lq = (int)q.size[2], d = (int)q.size[3];
     void *po, *pl, *pw;
-    PyObject *r[2], *ws = NULL;
-    r[0] = empty(4, q.size, type_of(q.code), q.dev, &po);
-    r[1] = empty(3, q.size, t_f32, q.dev, &pl);
-    int rc = -1;
+    at::Tensor r[2], ws;
+    r[0] = empty(4, q.size, q.code, q.dev, &po);
+    r[1] = empty(3, q.size, BA_F32, q.dev, &pl);
+    int rc;
     const size_t need = L.attn_window_fwd_workspace_size(B, Hq, Lq, d, q.code);
-    if (r[0] && r[1] && scratch(need, q.dev, &ws, &pw)) {
+    ws = scratch(need, q.dev, &pw);
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.attn_window_fwd(view(&q), view(&k), view(&v), B, Hq, (int)k.size[1], Lq, (int)k.size[2], d, q.code, off, window,
                                sinks, kpm, ld, scale, po, q.code, (float *)pl, pw, need, st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 2, r, ws);
+    return results(rc, 2, r);
 }
 
 /* (q, k, v, out, dout, lse, window, sinks, q_off, key_padding_mask, scale) -> (dq, dk, dv) */
-static PyObject *window_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *window_bwd(PyObject *const *a, Py_ssize_t na) {
     Ten q, k, v, o, g, l;
     int window, sinks, off;
     const uint8_t *kpm;
@@ -250,23 +223,24 @@ static PyObject *window_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     const int B = (int)q.size[0], Hq = (int)q.size[1], Hkv = (int)k.size[1], Lq = (int)q.size[2], Lk = (int)k.size[2],
               d = (int)q.size[3];
     void *p[3], *pw;
-    PyObject *r[3], *ws = NULL;
-    r[0] = empty(4, q.size, type_of(q.code), q.dev, &p[0]);
-    r[1] = empty(4, k.size, type_of(q.code), q.dev, &p[1]);
-    r[2] = empty(4, k.size, type_of(q.code), q.dev, &p[2]);
-    int rc = -1;
+    at::Tensor r[3], ws;
+    r[0] = empty(4, q.size, q.code, q.dev, &p[0]);
+    r[1] = empty(4, k.size, q.code, q.dev, &p[1]);
+    r[2] = empty(4, k.size, q.code, q.dev, &p[2]);
+    int rc;
     const size_t need = L.attn_window_bwd_workspace_size(B, Hq, Hkv, Lq, Lk, d, off, window, sinks);
-    if (r[0] && r[1] && r[2] && scratch(need, q.dev, &ws, &pw)) {
+    ws = scratch(need, q.dev, &pw);
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.attn_window_bwd(view(&q), view(&k), view(&v), view(&o), view(&g), (const float *)l.ptr, B, Hq, Hkv, Lq, Lk, d,
                                q.code, off, window, sinks, kpm, ld, scale, p[0], p[1], p[2], q.code, pw, need, st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 3, r, ws);
+    return results(rc, 3, r);
 }
 
 /* (q, k_cache, v_cache, window, sinks, lengths, scale) -> (out, lse) */
-static PyObject *window_decode(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *window_decode(PyObject *const *a, Py_ssize_t na) {
     Ten q, k, v;
     int window, sinks;
     const int32_t *len;
@@ -278,22 +252,33 @@ static PyObject *window_decode(PyObject *self, PyObject *const *a, Py_ssize_t na
         return other_way();
     const int B = (int)q.size[0], Hq = (int)q.size[1], Hkv = (int)k.size[1], S = (int)k.size[2], d = (int)q.size[3];
     void *po, *pl, *pw;
-    PyObject *r[2], *ws = NULL;
-    r[0] = empty(4, q.size, type_of(q.code), q.dev, &po);
-    r[1] = empty(3, q.size, t_f32, q.dev, &pl);
-    int rc = -1;
+    at::Tensor r[2], ws;
+    r[0] = empty(4, q.size, q.code, q.dev, &po);
+    r[1] = empty(3, q.size, BA_F32, q.dev, &pl);
+    int rc;
     const size_t need = L.attn_window_decode_workspace_size(B, Hq, Hkv, S, d, window, sinks);
-    if (r[0] && r[1] && scratch(need, q.dev, &ws, &pw)) {
+    ws = scratch(need, q.dev, &pw);
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.attn_window_decode_fwd(view(&q), view(&k), view(&v), B, Hq, Hkv, S, d, q.code, len, window, sinks, scale, po,
                                       q.code, (float *)pl, pw, need, st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 2, r, ws);
+    return results(rc, 2, r);
+}
+
+int ints(PyObject *t, long long *to) {
+    if (!t || !PyTuple_Check(t) || PyTuple_GET_SIZE(t) > 4) return -1;
+    const int n = (int)PyTuple_GET_SIZE(t);
+    for (int i = 0; i < n; ++i) {
+        to[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
+        if (to[i] == -1 && PyErr_Occurred()) return -1;
+    }
+    return n;
 }
 
 /* A KV4Cache: its sizes (B, H, S, d), layout and device. */
-static int read_cache(PyObject *x, long long *size, ba_kv4 *c, long *dev) {
+int read_cache(PyObject *x, long long *size, ba_kv4 *c, long *dev) {
     PyObject *o = PyObject_GetAttr(x, s_shape);
     const int n = ints(o, size);
     Py_XDECREF(o);
@@ -305,7 +290,7 @@ static int read_cache(PyObject *x, long long *size, ba_kv4 *c, long *dev) {
     const int ok = b.len == (Py_ssize_t)sizeof *c;
     if (ok) memcpy(c, b.buf, sizeof *c);
     PyBuffer_Release(&b);
-    if (!ok || !(o = PyObject_GetAttrString(x, "dev"))) return 0;
+    if (!ok || !(o = PyObject_GetAttr(x, s_dev))) return 0;
     *dev = PyLong_AsLong(o);
     Py_DECREF(o);
     for (int i = 0; i < 4; ++i)
@@ -314,7 +299,7 @@ static int read_cache(PyObject *x, long long *size, ba_kv4 *c, long *dev) {
 }
 
 /* (cache, k, v, start, counts) -> cache */
-static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *append(PyObject *const *a, Py_ssize_t na) {
     Ten k, v;
     long long z[4];
     ba_kv4 c;
@@ -335,32 +320,35 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t na) {
 }
 
 /* (cache, T, first, dtype) -> (k, v) */
-static PyObject *read_back(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *read_back(PyObject *const *a, Py_ssize_t na) {
     long long z[4];
     ba_kv4 c;
     long dev;
     int T, first;
     ba_stream_t st;
     if (na != 4 || !read_cache(a[0], z, &c, &dev) || !whole(a[1], 0, &T) || !whole(a[2], 0, &first) ||
-        (a[3] != t_bf16 && a[3] != t_f32) || !stream_of(dev, &st))
+        !THPDtype_Check(a[3]) || !stream_of(dev, &st))
         return other_way();
+    const at::ScalarType type = reinterpret_cast<THPDtype *>(a[3])->scalar_type;
+    if (type != at::kBFloat16 && type != at::kFloat) return other_way();
+    const int code = type == at::kBFloat16 ? BA_BF16 : BA_F32;
     const int S = (int)z[2];
     z[2] = T;
     void *p[2];
-    PyObject *r[2];
-    r[0] = empty(4, z, a[3], dev, &p[0]);
-    r[1] = empty(4, z, a[3], dev, &p[1]);
-    int rc = -1;
-    if (r[0] && r[1]) {
+    at::Tensor r[2];
+    r[0] = empty(4, z, code, dev, &p[0]);
+    r[1] = empty(4, z, code, dev, &p[1]);
+    int rc;
+    {
         Py_BEGIN_ALLOW_THREADS
-        rc = L.kv4_read(c, (int)z[0], (int)z[1], S, (int)z[3], first, T, a[3] == t_bf16 ? BA_BF16 : BA_F32, p[0], p[1], st);
+        rc = L.kv4_read(c, (int)z[0], (int)z[1], S, (int)z[3], first, T, code, p[0], p[1], st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 2, r, NULL);
+    return results(rc, 2, r);
 }
 
 /* (q, cache, lengths, window, sinks, scale) -> (out, lse) */
-static PyObject *decode_kv4(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *decode_kv4(PyObject *const *a, Py_ssize_t na) {
     Ten q;
     long long z[4];
     ba_kv4 c;
@@ -376,18 +364,19 @@ static PyObject *decode_kv4(PyObject *self, PyObject *const *a, Py_ssize_t na) {
         return other_way();
     const int B = (int)z[0], Hq = (int)q.size[1], Hkv = (int)z[1], S = (int)z[2], d = (int)z[3];
     void *po, *pl, *pw;
-    PyObject *r[2], *ws = NULL;
-    r[0] = empty(4, q.size, type_of(q.code), dev, &po);
-    r[1] = empty(3, q.size, t_f32, dev, &pl);
-    int rc = -1;
+    at::Tensor r[2], ws;
+    r[0] = empty(4, q.size, q.code, dev, &po);
+    r[1] = empty(3, q.size, BA_F32, dev, &pl);
+    int rc;
     const size_t need = L.attn_decode_kv4_workspace_size(B, Hq, Hkv, S, d, window, sinks);
-    if (r[0] && r[1] && scratch(need, dev, &ws, &pw)) {
+    ws = scratch(need, dev, &pw);
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.attn_decode_kv4_fwd(view(&q), c, B, Hq, Hkv, S, d, q.code, len, window, sinks, scale, po, q.code, (float *)pl, pw,
                                    need, st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 2, r, ws);
+    return results(rc, 2, r);
 }
 
 /* What the norm's two directions share: q, k, wq, wk, eps, positions, base, pos_scale. */
@@ -399,7 +388,7 @@ typedef struct {
     ba_stream_t st;
 } Norm;
 
-static int read_norm(PyObject *const *a, Norm *n) {
+int read_norm(PyObject *const *a, Norm *n) {
     if (!read_tensor(a[0], &n->q) || !read_tensor(a[1], &n->k) || !heads(&n->q) || !heads(&n->k) || !fits(&n->q) || !fits(&n->k))
         return 0;
     const Ten *q = &n->q, *k = &n->k;
@@ -414,7 +403,7 @@ static int read_norm(PyObject *const *a, Norm *n) {
     n->eps = (float)PyFloat_AS_DOUBLE(a[4]);
     n->base = (float)PyFloat_AS_DOUBLE(a[6]);
     n->scale = (float)PyFloat_AS_DOUBLE(a[7]);
-    n->pos = NULL;
+    n->pos = nullptr;
     n->ld = 0;
     if (a[5] != Py_None) {
         Ten p;
@@ -432,26 +421,26 @@ static int read_norm(PyObject *const *a, Norm *n) {
 }
 
 /* (q, k, wq, wk, eps, positions, base, pos_scale) -> (yq, yk) */
-static PyObject *norm_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *norm_fwd(PyObject *const *a, Py_ssize_t na) {
     Norm n;
     if (na != 8 || !read_norm(a, &n)) return other_way();
     void *p[2];
-    PyObject *r[2];
-    r[0] = empty(4, n.q.size, type_of(n.q.code), n.q.dev, &p[0]);
-    r[1] = empty(4, n.k.size, type_of(n.q.code), n.q.dev, &p[1]);
-    int rc = -1;
-    if (r[0] && r[1]) {
+    at::Tensor r[2];
+    r[0] = empty(4, n.q.size, n.q.code, n.q.dev, &p[0]);
+    r[1] = empty(4, n.k.size, n.q.code, n.q.dev, &p[1]);
+    int rc;
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.qk_norm_rope_fwd(view(&n.q), view(&n.k), n.wq.ptr, n.wk.ptr, n.wq.code, (int)n.q.size[0], (int)n.q.size[1],
                                 (int)n.k.size[1], (int)n.q.size[2], (int)n.q.size[3], n.q.code, n.eps, n.pos, n.ld, n.base,
                                 n.scale, p[0], p[1], n.st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 2, r, NULL);
+    return results(rc, 2, r);
 }
 
 /* (q, k, wq, wk, eps, positions, base, pos_scale, dyq, dyk) -> (dq, dk, dwq, dwk) */
-static PyObject *norm_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+PyObject *norm_bwd(PyObject *const *a, Py_ssize_t na) {
     Norm n;
     Ten gq, gk;
     if (na != 10 || !read_norm(a, &n) || !read_tensor(a[8], &gq) || !read_tensor(a[9], &gk) || !heads(&gq) || !heads(&gk) ||
@@ -462,33 +451,33 @@ static PyObject *norm_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     const int B = (int)n.q.size[0], Hq = (int)n.q.size[1], Hkv = (int)n.k.size[1], T = (int)n.q.size[2], d = (int)n.q.size[3];
     const long long row = d;
     void *p[4], *pw;
-    PyObject *r[4], *ws = NULL;
-    r[0] = empty(4, n.q.size, type_of(n.q.code), n.q.dev, &p[0]);
-    r[1] = empty(4, n.k.size, type_of(n.q.code), n.q.dev, &p[1]);
-    r[2] = empty(1, &row, t_f32, n.q.dev, &p[2]);
-    r[3] = empty(1, &row, t_f32, n.q.dev, &p[3]);
-    int rc = -1;
+    at::Tensor r[4], ws;
+    r[0] = empty(4, n.q.size, n.q.code, n.q.dev, &p[0]);
+    r[1] = empty(4, n.k.size, n.q.code, n.q.dev, &p[1]);
+    r[2] = empty(1, &row, BA_F32, n.q.dev, &p[2]);
+    r[3] = empty(1, &row, BA_F32, n.q.dev, &p[3]);
+    int rc;
     const size_t need = L.qk_norm_rope_bwd_workspace_size(B, Hq, Hkv, T, d, n.q.code);
-    if (r[0] && r[1] && r[2] && r[3] && scratch(need, n.q.dev, &ws, &pw)) {
+    ws = scratch(need, n.q.dev, &pw);
+    {
         Py_BEGIN_ALLOW_THREADS
         rc = L.qk_norm_rope_bwd(view(&n.q), view(&n.k), n.wq.ptr, n.wk.ptr, n.wq.code, view(&gq), view(&gk), gq.code, B, Hq, Hkv,
                                 T, d, n.q.code, n.eps, n.pos, n.ld, n.base, n.scale, p[0], p[1], (float *)p[2], (float *)p[3], pw,
                                 need, n.st);
         Py_END_ALLOW_THREADS
     }
-    return results(rc, 4, r, ws);
+    return results(rc, 4, r);
 }
 
-/* bind({entry point: address}, torch.empty, bfloat16, float32, uint8, int32, current device, current stream) */
-static PyObject *bind(PyObject *self, PyObject *args) {
-    PyObject *d, *o[7];
-    if (!PyArg_ParseTuple(args, "O!OOOOOOO", &PyDict_Type, &d, &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6])) return NULL;
+/* bind({entry point: address}) */
+PyObject *bind(PyObject *, PyObject *d) {
+    if (!PyDict_Check(d)) return PyErr_Format(PyExc_TypeError, "expected a dict of addresses");
 #define ADDRESS(name)                                                                                                    \
     do {                                                                                                                 \
         PyObject *x = PyDict_GetItemString(d, #name);                                                                    \
         if (!x) return PyErr_Format(PyExc_KeyError, "%s", #name);                                                        \
-        L.name = (__typeof__(L.name))PyLong_AsVoidPtr(x);                                                                \
-        if (PyErr_Occurred()) return NULL;                                                                               \
+        L.name = reinterpret_cast<decltype(L.name)>(PyLong_AsVoidPtr(x));                                                \
+        if (PyErr_Occurred()) return nullptr;                                                                            \
     } while (0)
     ADDRESS(attn_window_fwd);
     ADDRESS(attn_window_fwd_workspace_size);
@@ -503,35 +492,39 @@ static PyObject *bind(PyObject *self, PyObject *args) {
     ADDRESS(qk_norm_rope_fwd);
     ADDRESS(qk_norm_rope_bwd);
     ADDRESS(qk_norm_rope_bwd_workspace_size);
-    PyObject **to[7] = {&t_empty, &t_bf16, &t_f32, &t_u8, &t_i32, &t_device, &t_stream};
-    for (int i = 0; i < 7; ++i) {
-        Py_INCREF(o[i]);
-        Py_XSETREF(*to[i], o[i]);
-    }
     Py_RETURN_NONE;
 }
 
-#define FAST(f) (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL
-static PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, NULL},
-                                {"attn_window_fwd", FAST(window_fwd)},
-                                {"attn_window_bwd", FAST(window_bwd)},
-                                {"attn_window_decode_fwd", FAST(window_decode)},
-                                {"kv4_append", FAST(append)},
-                                {"kv4_read", FAST(read_back)},
-                                {"attn_decode_kv4_fwd", FAST(decode_kv4)},
-                                {"qk_norm_rope_fwd", FAST(norm_fwd)},
-                                {"qk_norm_rope_bwd", FAST(norm_bwd)},
-                                {NULL, NULL, 0, NULL}};
-static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
+// No exception passes into the interpreter (torch throws when memory runs out; the Python
+// function meets the same and raises it).
+template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
+PyObject *call(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    try {
+        return F(a, na);
+    } catch (...) {
+        return other_way();
+    }
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(call<f>)), METH_FASTCALL, nullptr
+PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
+                         {"attn_window_fwd", FAST(window_fwd)},
+                         {"attn_window_bwd", FAST(window_bwd)},
+                         {"attn_window_decode_fwd", FAST(window_decode)},
+                         {"kv4_append", FAST(append)},
+                         {"kv4_read", FAST(read_back)},
+                         {"attn_decode_kv4_fwd", FAST(decode_kv4)},
+                         {"qk_norm_rope_fwd", FAST(norm_fwd)},
+                         {"qk_norm_rope_bwd", FAST(norm_bwd)},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
 
 PyMODINIT_FUNC PyInit__fastcall(void) {
     s_shape = PyUnicode_InternFromString("shape");
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_stride = PyUnicode_InternFromString("stride");
-    s_ptr = PyUnicode_InternFromString("data_ptr");
-    s_dev = PyUnicode_InternFromString("get_device");
+    s_dev = PyUnicode_InternFromString("dev");
     s_c = PyUnicode_InternFromString("_c");
-    kw_empty = Py_BuildValue("(ss)", "dtype", "device");
-    if (!s_shape || !s_dtype || !s_stride || !s_ptr || !s_dev || !s_c || !kw_empty) return NULL;
+    if (!s_shape || !s_dev || !s_c) return nullptr;
     return PyModule_Create(&module);
 }

@@ -1,4 +1,4 @@
-"""The calls marshalled in C give what the same calls give through the Python binding, bit
+"""The calls marshalled in C++ give what the same calls give through the Python binding, bit
 for bit, and whatever they do not know goes on to the Python binding's checks."""
 import pytest
 import torch
