@@ -1859,6 +1859,9 @@ bool window_tma_ok(const ba_tensor &t, int B, int H) {
     return tma_ok(t, B, H) && t.sT > 0 && (H <= 1 || t.sH > 0) && (B <= 1 || t.sB > 0);
 }
 
+// Keys behind the last query (free slots of a cache, which may hold anything) are not read.
+int keys_up_to(long long last, int Lk) { return Lk < last ? Lk : (int)last; }
+
 int window_heads_per_group(int B, int Hq, int Hkv, long long keys, int d, int dtype) {
     return heads_per_group(B, Hkv, keys, d, dtype) * (Hq / Hkv);
 }
@@ -1889,6 +1892,7 @@ int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v, int B, int Hq, int Hk
     const int dev = current_device();
     if (dev < 0) return BA_ERR_CUDA;
     if ((rc = device_setup(dev))) return rc;
+    Lk = keys_up_to(q_off + Lq, Lk);
     q = fix_unit_strides(q, B, Hq, Lq, d);
     k = fix_unit_strides(k, B, Hkv, Lk, d);
     v = fix_unit_strides(v, B, Hkv, Lk, d);
@@ -2035,8 +2039,9 @@ int attn_window_bwd(ba_tensor q, ba_tensor k, ba_tensor v, ba_tensor out, ba_ten
     ba::BwdMaps m;
     if ((rc = encode_map(&m.q, q.ptr, d, Lq, Hq, B, q.sT, q.sH, q.sB))) return rc;
     if ((rc = encode_map(&m.dout, dout.ptr, d, Lq, Hq, B, dout.sT, dout.sH, dout.sB))) return rc;
-    if ((rc = encode_map(&m.k, k.ptr, d, Lk, Hkv, B, k.sT, k.sH, k.sB))) return rc;
-    if ((rc = encode_map(&m.v, v.ptr, d, Lk, Hkv, B, v.sT, v.sH, v.sB))) return rc;
+    const int seen = keys_up_to(q_off + Lq, Lk);
+    if ((rc = encode_map(&m.k, k.ptr, d, seen, Hkv, B, k.sT, k.sH, k.sB))) return rc;
+    if ((rc = encode_map(&m.v, v.ptr, d, seen, Hkv, B, v.sT, v.sH, v.sB))) return rc;
     return ba::launch_attn_window_bwd_tc(a, m, g_num_sms[dev], stream);
 }
 
@@ -2312,6 +2317,9 @@ int kv4_append(ba_tensor k, ba_tensor v, ba_kv4 cache, int B, int H, int T, int 
     if (d != 64 && d != 128) return BA_ERR_SHAPE;
     if ((long long)B * H * T == 0 || S == 0) return BA_OK;
     if (!kv4_ok(cache, B, H, d)) return BA_ERR_ARG;
+    if ((B > 1 && (!cache.codes_sB || !cache.scales_sB)) || (H > 1 && (!cache.codes_sH || !cache.scales_sH)) ||
+        (S > 1 && (!cache.codes_sT || !cache.scales_sT)))
+        return BA_ERR_ARG;   // several rows in one place
     const size_t eb = elem_size(dtype);
     ba::Kv4Args a;
     std::memset(&a, 0, sizeof a);

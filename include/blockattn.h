@@ -293,7 +293,9 @@ int ulysses_attn_fwd(const void *q_tok, const void *k_tok, const void *v_tok,
  *    CUDA cores in fp32).
  *  window >= 1, sinks >= 0.
  *  key_padding_mask: NULL or uint8 (B, >= Lk), 1 = excluded; what K and V hold at
- *    an excluded key has no effect, infinities and NaN included.
+ *    an excluded key, or behind the last query, has no effect, infinities and NaN
+ *    included.  (At other keys they reach the rows of the same tile of 128, as 0 times
+ *    them does in the formula.)
  *  scale: > 0, or <= 0 for 1/sqrt(d).
  *  out: (B, Hq, Lq, d) contiguous, 16-byte aligned, out_dtype = BA_F32 or dtype;
  *    lse: (B, Hq, Lq) fp32.  A row that sees no key gets out = 0, lse = -inf.
@@ -319,7 +321,8 @@ int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v,
  *  out, dout: (B, Hq, Lq, d), dtype; lse: the forward's.  Everything else as for
  *    the forward.  q, out and dout hold finite values.
  *  dq: (B, Hq, Lq, d); dk, dv: (B, Hkv, Lk, d), contiguous, overwritten, grad_dtype
- *    = BA_F32 or dtype (sums in fp32, rounded once).
+ *    = BA_F32 or dtype (sums in fp32, rounded once; on the tensor cores P and dS are
+ *    rounded to bf16 for their products).
  *  workspace: attn_window_bwd_workspace_size() bytes: D_i per row, and for the key
  *    tiles that hold sinks (seen by every later query) fp32 partials over chunks of
  *    the queries, added in a fixed order.  No atomics: equal calls give equal bits.
@@ -405,6 +408,7 @@ typedef struct {
  * they hold.
  *  k, v: (B, H, T, d) of dtype BA_F32 or BA_BF16, strided, rows on 16-byte boundaries.
  *  start: NULL (0) or device int32[B]; counts: NULL (T) or device int32[B].
+ *  The cache's rows lie in places of their own (BA_ERR_ARG for strides of 0).
  * kv4_read -- the values of the slots first .. first + T - 1 (0 <= first,
  * first + T <= S) as contiguous (B, H, T, d) tensors of dtype (bf16 holds them exactly
  * while they are normal numbers: 6 significant bits).
@@ -462,8 +466,9 @@ int rope_apply(ba_tensor x, ba_tensor x2, int B, int H, int T, int d, int dtype,
  *  positions: NULL (position of row t is t), or device int32: entry (b, t) at
  *    positions[b * positions_ld + t]; positions_ld = 0: one row shared by all sequences.
  *  base, pos_scale: as for rope_apply.
- *  yq: (B, Hq, T, d), yk: (B, Hkv, T, d): contiguous, 16-byte aligned, dtype; computed
- *    in fp32 (the angles in fp64) and rounded once.
+ *  yq: (B, Hq, T, d), yk: (B, Hkv, T, d): contiguous, 16-byte aligned, dtype, not
+ *    overlapping the inputs; computed in fp32 (the angles as 64-bit fractions of a turn)
+ *    and rounded once.
  * qk_norm_rope_bwd -- the gradients for dyq, dyk (shapes of q and k, strided, dy_dtype =
  *  BA_F32 or dtype): dq, dk contiguous of dtype; dwq, dwk (d) fp32, summed over all
  *  rows in a fixed order.  workspace: qk_norm_rope_bwd_workspace_size() bytes.

@@ -202,3 +202,13 @@ def test_binding_refusals():
         ba.attn_window_bwd(q, k, v, out, g, lse, window=8, dk=torch.empty_like(q))
     with pytest.raises(ba.BlockAttnError):   # a workspace that is too small
         ba.attn_window_bwd(q, k, v, out, g, lse, window=8, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("bf16", 64), ("f32", 64), ("bf16", 32)])
+@pytest.mark.parametrize("q_off,Lk", [(0, 300), (70, 512), (201, 500)])
+def test_free_slots_behind_the_last_query(dt, d, q_off, Lk):
+    """A chunk of 150 queries on a cache with free slots: NaN and infinities there have no effect."""
+    q, k, v, g = inputs(2, 4, 2, 150, Lk, d, dt, 120)
+    k[:, :, q_off + 150:], v[:, :, q_off + 150:] = math.nan, math.inf
+    _, _, (_, dk, dv) = both(q, k, v, g, window=100, sinks=3, q_off=q_off, label=f"free slots {dt} {q_off}")
+    assert (dk[:, :, q_off + 150:] == 0).all() and (dv[:, :, q_off + 150:] == 0).all()

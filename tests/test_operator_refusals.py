@@ -130,3 +130,10 @@ def test_qk_norm():
                                     0, None)
     assert bwd(dwq=None) == BA_ERR_ARG and bwd(gdt=9) == BA_ERR_ARG
     assert 0 < lib.qk_norm_rope_bwd_workspace_size(2, 16, 4, 8192, 128, BF) <= 1 << 21
+
+
+@pytest.mark.parametrize("stride", ["codes_sB", "codes_sH", "codes_sT", "scales_sB", "scales_sH", "scales_sT"])
+def test_kv4_append_wants_rows_in_places_of_their_own(stride):
+    lib = ba.load()
+    c = cache(**{stride: 0})
+    assert lib.kv4_append(X, X, c, 2, 2, 1, 8, 64, BF, None, None, None) == BA_ERR_ARG
