@@ -2030,7 +2030,7 @@ int attn_window_bwd(ba_tensor q, ba_tensor k, ba_tensor v, ba_tensor out, ba_ten
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };   // 16-byte stores
     const bool tc = ba::bwd_tc_supported(dtype, d) && window_tma_ok(q, B, Hq) && window_tma_ok(k, B, Hkv) &&
                     window_tma_ok(v, B, Hkv) && window_tma_ok(dout, B, Hq) && al16(dq) && al16(dk) && al16(dv);
-    const SinkParts p = sink_parts(w, Lq, tc ? TILE : 64);
+    const SinkParts p = sink_parts(w, Lq, tc ? TILE : ba::WINDOW_SIMT_ROWS);
     a.n_sink_tiles = p.tiles;
     a.n_sink_parts = p.parts;
     a.sink_rows = p.rows;

@@ -167,49 +167,11 @@ __device__ __forceinline__ int partner_spans(const BwdArgs &a, const Tile &x, bo
     return n;
 }
 
-template <bool W>
 __device__ __forceinline__ bool is_excluded(const BwdArgs &a, int b, long long qp, long long kp) {
     if (a.causal && kp > qp) return true;
-    if (W && kp <= qp - a.window && kp >= a.sinks) return true;
     if (a.kpm && a.kpm[b * a.kpm_ld + kp]) return true;
     if (a.am && a.am[qp * a.am_ld + kp]) return true;
     return false;
-}
-
-// Sliding window with sinks (W): the key ranges of a query tile (the sinks before
-// the window, then the window), and the query rows of a key tile, taken once for
-// each query head of the group; `part` >= 0 restricts those to one chunk (key tiles
-// that hold sinks, whose queries are the whole sequence behind them).
-__device__ __forceinline__ int window_q_spans(const BwdArgs &a, const Tile &x, Span *sp) {
-    const long long end = min(x.pos0 + x.len, (long long)a.Lk), lo = max(0LL, x.pos0 - a.window + 1);
-    int n = 0;
-    if (lo > a.sinks) {
-        sp[n++] = Span{0, min((long long)a.sinks, end), 0};
-        sp[n++] = Span{lo, end, lo};
-    } else {
-        sp[n++] = Span{0, end, 0};
-    }
-    return n;
-}
-
-__device__ __forceinline__ Span window_k_span(const BwdArgs &a, const Tile &x, int part) {
-    long long lo = x.pos0 - a.q_off, hi = x.pos0 + x.len - 1 + a.window - a.q_off;
-    if (part >= 0) {
-        lo = max(lo, (long long)part * a.sink_rows);
-        hi = (long long)(part + 1) * a.sink_rows;
-    } else if (x.pos0 < a.sinks) {
-        hi = a.Lq;   // sinks taken whole: one chunk covers every query
-    }
-    lo = max(lo, 0LL);
-    return Span{lo, min(hi, (long long)a.Lq), lo + a.q_off};
-}
-
-// A gradient element, of either type (bf16: rounded once, here).
-__device__ __forceinline__ void put_grad(const BwdArgs &a, void *base, long long i, float v) {
-    if (a.grad_bf16)
-        static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<float *>(base)[i] = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -223,26 +185,15 @@ __host__ __device__ inline size_t dkdv_smem_bytes(int d) {
     return sizeof(float) * ((size_t)2 * BT * (d + 1) + (size_t)2 * BC * (d + 1) + (size_t)2 * BC * (BT + 1) + 2 * BC);
 }
 
-template <int D, bool W>
+template <int D>
 __global__ void __launch_bounds__(NTH) bwd_dkdv_kernel(const BwdArgs a) {
     extern __shared__ float smf[];
     constexpr int LD = D + 1;
     float *Ks = smf, *Vs = Ks + BT * LD, *Qs = Vs + BT * LD, *Gs = Qs + BC * LD;
     float *Ps = Gs + BC * LD, *Ss = Ps + BC * (BT + 1), *lse_s = Ss + BC * (BT + 1), *D_s = lse_s + BC;
     const int t = threadIdx.x;
-    const int n_heads = W ? a.Hkv : a.H;
-    const int bh = blockIdx.y, b = bh / n_heads, h = bh % n_heads;
-    int tile = blockIdx.x, part = -1;
-    if (W) {
-        const int parts = a.n_sink_tiles * a.n_sink_parts;
-        if (tile < parts) {
-            part = tile % a.n_sink_parts;
-            tile /= a.n_sink_parts;
-        } else {
-            tile += a.n_sink_tiles - parts;
-        }
-    }
-    const Tile kt = make_tile(a, tile, false);
+    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    const Tile kt = make_tile(a, blockIdx.x, false);
     const long long q_rows = a.ring ? a.T : a.Lq;
 
     for (int e = t; e < BT * D; e += NTH) {
@@ -267,15 +218,10 @@ __global__ void __launch_bounds__(NTH) bwd_dkdv_kernel(const BwdArgs a) {
     const float sl2 = a.scale * 1.4426950408889634f;
     const long long k_last = kt.pos0 + kt.len - 1;
 
-    const int steps = W ? a.kv_group : (a.ring ? a.s_end - a.s_begin : 1);
+    const int steps = a.ring ? a.s_end - a.s_begin : 1;
     for (int st = 0; st < steps; ++st) {
         Span sp[2];
-        int nsp = 1;
-        if constexpr (W)
-            sp[0] = window_k_span(a, kt, part);
-        else
-            nsp = partner_spans(a, kt, false, a.ring ? a.s_begin + st : 0, sp);
-        const int hq = W ? h * a.kv_group + st : h;   // query head of this step
+        const int nsp = partner_spans(a, kt, false, a.ring ? a.s_begin + st : 0, sp);
         for (int si_ = 0; si_ < nsp; ++si_) {
             long long r0 = sp[si_].row0;
             const long long r1 = sp[si_].row1, dpos = sp[si_].pos0 - sp[si_].row0;
@@ -288,14 +234,14 @@ __global__ void __launch_bounds__(NTH) bwd_dkdv_kernel(const BwdArgs a) {
                     const int i = e / D, c = e % D;
                     float qv = 0.f, gv = 0.f;
                     if (i < qn) {
-                        qv = ld_elem(a.q.p, a.dtype, elem_index(a.q, b, hq, q0 + i, c));
-                        gv = ld_elem(a.dout.p, a.dtype, elem_index(a.dout, b, hq, q0 + i, c));
+                        qv = ld_elem(a.q.p, a.dtype, elem_index(a.q, b, h, q0 + i, c));
+                        gv = ld_elem(a.dout.p, a.dtype, elem_index(a.dout, b, h, q0 + i, c));
                     }
                     Qs[i * LD + c] = qv;
                     Gs[i * LD + c] = gv;
                 }
                 if (t < BC) {
-                    const long long row = ((long long)b * a.H + hq) * q_rows + q0 + t;
+                    const long long row = (long long)bh * q_rows + q0 + t;
                     lse_s[t] = t < qn ? a.lse[row] : -INFINITY;
                     D_s[t] = t < qn ? a.D[row] : 0.f;
                 }
@@ -318,7 +264,7 @@ __global__ void __launch_bounds__(NTH) bwd_dkdv_kernel(const BwdArgs a) {
                     for (int r = 0; r < 4; ++r) {
                         const int j = sj + 16 * r;
                         float p = 0.f, ds = 0.f;
-                        if (si < qn && j < kt.len && L != -INFINITY && !is_excluded<W>(a, b, qp, kt.pos0 + j)) {
+                        if (si < qn && j < kt.len && L != -INFINITY && !is_excluded(a, b, qp, kt.pos0 + j)) {
                             p = exp2f(fmaf(s4[r], sl2, -L * 1.4426950408889634f));
                             ds = p * (g4[r] - D_s[si]);
                         }
@@ -342,26 +288,6 @@ __global__ void __launch_bounds__(NTH) bwd_dkdv_kernel(const BwdArgs a) {
             }
         }
     }
-    if constexpr (W) {
-        if (jo >= kt.len) return;
-        if (part >= 0) {   // dV, then dK of the chunk's partial
-            float *dst = a.part +
-                         ((((long long)bh * a.n_sink_tiles + tile) * a.n_sink_parts + part) * 2 * BT + jo) * (long long)D;
-#pragma unroll
-            for (int m = 0; m < NCOL; ++m) {
-                dst[co + 4 * m] = dv[m];
-                dst[(long long)BT * D + co + 4 * m] = dk[m] * a.scale;
-            }
-        } else {
-            const long long row = ((long long)bh * a.Lk + kt.row0 + jo) * D;
-#pragma unroll
-            for (int m = 0; m < NCOL; ++m) {
-                put_grad(a, a.dv, row + co + 4 * m, dv[m]);
-                put_grad(a, a.dk, row + co + 4 * m, dk[m] * a.scale);
-            }
-        }
-        return;
-    }
     if (jo < kt.len) {
         const long long row = ((long long)bh * (a.ring ? a.T : a.Lk) + kt.row0 + jo) * D;
 #pragma unroll
@@ -384,7 +310,7 @@ __host__ __device__ inline size_t dq_smem_bytes(int d) {
     return sizeof(float) * ((size_t)2 * BT * (d + 1) + (size_t)2 * BC * (d + 1) + (size_t)BT * (BC + 1) + 2 * BT);
 }
 
-template <int D, bool W>
+template <int D>
 __global__ void __launch_bounds__(NTH) bwd_dq_kernel(const BwdArgs a) {
     extern __shared__ float smf[];
     constexpr int LD = D + 1;
@@ -421,11 +347,10 @@ __global__ void __launch_bounds__(NTH) bwd_dq_kernel(const BwdArgs a) {
     const float sl2 = a.scale * 1.4426950408889634f;
     const long long q_last = qt.pos0 + qt.len - 1;
 
-    const int kvh = W ? h / a.kv_group : h;
     const int steps = a.ring ? a.s_end - a.s_begin : 1;
     for (int st = 0; st < steps; ++st) {
         Span sp[2];
-        const int nsp = W ? window_q_spans(a, qt, sp) : partner_spans(a, qt, true, a.ring ? a.s_begin + st : 0, sp);
+        const int nsp = partner_spans(a, qt, true, a.ring ? a.s_begin + st : 0, sp);
         for (int s_ = 0; s_ < nsp; ++s_) {
             const long long r0 = sp[s_].row0, dpos = sp[s_].pos0 - sp[s_].row0;
             long long r1 = sp[s_].row1;
@@ -437,10 +362,9 @@ __global__ void __launch_bounds__(NTH) bwd_dq_kernel(const BwdArgs a) {
                 for (int e = t; e < BC * D; e += NTH) {
                     const int j = e / D, c = e % D;
                     float kv = 0.f, vv = 0.f;
-                    // (window: a padded key's rows may hold anything and are not read)
-                    if (j < kn && !(W && a.kpm && a.kpm[b * a.kpm_ld + k0 + j])) {
-                        kv = ld_elem(a.k.p, a.dtype, elem_index(a.k, b, kvh, k0 + j, c));
-                        vv = ld_elem(a.v.p, a.dtype, elem_index(a.v, b, kvh, k0 + j, c));
+                    if (j < kn) {
+                        kv = ld_elem(a.k.p, a.dtype, elem_index(a.k, b, h, k0 + j, c));
+                        vv = ld_elem(a.v.p, a.dtype, elem_index(a.v, b, h, k0 + j, c));
                     }
                     Ks[j * LD + c] = kv;
                     Vs[j * LD + c] = vv;
@@ -463,7 +387,7 @@ __global__ void __launch_bounds__(NTH) bwd_dq_kernel(const BwdArgs a) {
                         const int i = si + 16 * r;
                         const float L = lse_s[i];
                         float ds = 0.f;
-                        if (sj < kn && i < qt.len && L != -INFINITY && !is_excluded<W>(a, b, qt.pos0 + i, kp)) {
+                        if (sj < kn && i < qt.len && L != -INFINITY && !is_excluded(a, b, qt.pos0 + i, kp)) {
                             const float p = exp2f(fmaf(s4[r], sl2, -L * 1.4426950408889634f));
                             ds = p * (g4[r] - D_s[i]);
                         }
@@ -486,13 +410,17 @@ __global__ void __launch_bounds__(NTH) bwd_dq_kernel(const BwdArgs a) {
         for (int m = 0; m < NCOL; ++m) {
             const int c = co + 4 * m;
             const float g = dq[m] * a.scale;
-            if constexpr (W) {
-                put_grad(a, a.dq, row + c, g);
-                continue;
-            }
             a.dq[row + c] = a.accumulate ? a.dq[row + c] + g : g;
         }
     }
+}
+
+// A gradient element, of either type (bf16: rounded once, here).
+__device__ __forceinline__ void put_grad(const BwdArgs &a, void *base, long long i, float v) {
+    if (a.grad_bf16)
+        static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(base)[i] = v;
 }
 
 // One thread per four columns of a row of dV or dK in a key tile that holds sinks.
@@ -522,21 +450,16 @@ __global__ void __launch_bounds__(256) sink_sum_kernel(const BwdArgs a, int tile
     }
 }
 
-template <int D, bool W>
+template <int D>
 int launch_d(const BwdArgs &a, int n_qt, int n_kt, cudaStream_t s) {
     const size_t s1 = dkdv_smem_bytes(D), s2 = dq_smem_bytes(D);
-    if (cudaFuncSetAttribute(bwd_dkdv_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1) !=
+    if (cudaFuncSetAttribute(bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(bwd_dq_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2) != cudaSuccess)
+        cudaFuncSetAttribute(bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2) != cudaSuccess)
         return BA_ERR_CUDA;
     const int BH = a.B * a.H;
-    if constexpr (W) {
-        const int items = n_kt - a.n_sink_tiles + a.n_sink_tiles * a.n_sink_parts;
-        if (n_kt > 0) bwd_dkdv_kernel<D, W><<<dim3(items, a.B * a.Hkv), NTH, s1, s>>>(a);
-    } else {
-        if (n_kt > 0) bwd_dkdv_kernel<D, W><<<dim3(n_kt, BH), NTH, s1, s>>>(a);
-    }
-    if (n_qt > 0) bwd_dq_kernel<D, W><<<dim3(n_qt, BH), NTH, s2, s>>>(a);
+    if (n_kt > 0) bwd_dkdv_kernel<D><<<dim3(n_kt, BH), NTH, s1, s>>>(a);
+    if (n_qt > 0) bwd_dq_kernel<D><<<dim3(n_qt, BH), NTH, s2, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
 }
 
@@ -565,10 +488,10 @@ int launch_attn_bwd(const BwdArgs &a, int num_sms, cudaStream_t s) {
         if (rc) return rc;
     }
     switch (a.d) {
-        case 16: return launch_d<16, false>(a, n_qt, n_kt, s);
-        case 32: return launch_d<32, false>(a, n_qt, n_kt, s);
-        case 64: return launch_d<64, false>(a, n_qt, n_kt, s);
-        case 128: return launch_d<128, false>(a, n_qt, n_kt, s);
+        case 16: return launch_d<16>(a, n_qt, n_kt, s);
+        case 32: return launch_d<32>(a, n_qt, n_kt, s);
+        case 64: return launch_d<64>(a, n_qt, n_kt, s);
+        case 128: return launch_d<128>(a, n_qt, n_kt, s);
         default: return BA_ERR_SHAPE;
     }
 }
@@ -600,25 +523,6 @@ int launch_window_pre(const BwdArgs &a, int num_sms, cudaStream_t s) {
         if (reinterpret_cast<uintptr_t>(t->p) % 16 || t->sB * e % 16 || t->sH * e % 16 || t->sT * e % 16)
             return launch_bwd_pre(a, num_sms, s);
     return a.dtype == BA_BF16 ? launch_window_pre_t<__nv_bfloat16>(a, rows, s) : launch_window_pre_t<float>(a, rows, s);
-}
-
-// The window form: D, the same kernels over the window's spans, and the sum of the
-// sink tiles' partials.
-int launch_attn_window_bwd(const BwdArgs &a, int num_sms, cudaStream_t s) {
-    const int BH = a.B * a.H;
-    if (BH == 0) return BA_OK;
-    if (BH > 65535) return BA_ERR_SHAPE;
-    const int n_qt = (a.Lq + BT - 1) / BT, n_kt = (a.Lk + BT - 1) / BT;
-    int rc = launch_window_pre(a, num_sms, s);
-    if (rc) return rc;
-    switch (a.d) {
-        case 16: rc = launch_d<16, true>(a, n_qt, n_kt, s); break;
-        case 32: rc = launch_d<32, true>(a, n_qt, n_kt, s); break;
-        case 64: rc = launch_d<64, true>(a, n_qt, n_kt, s); break;
-        case 128: rc = launch_d<128, true>(a, n_qt, n_kt, s); break;
-        default: rc = BA_ERR_SHAPE;
-    }
-    return rc ? rc : launch_sink_sum(a, BT, num_sms, s);
 }
 
 // dV / dK rows of the key tiles (of `tile_rows` rows) that hold sinks: the sum of

@@ -220,6 +220,286 @@ int launch_d(const AttnArgs &a, long long blocks, cudaStream_t s) {
     return a.dtype == BA_F32 ? launch_t<D, float>(a, blocks, s) : launch_t<D, __nv_bfloat16>(a, blocks, s);
 }
 
+// ---------------------------------------------------------------------------
+// Gradients
+// ---------------------------------------------------------------------------
+
+// dS = P * (dO V^T - D) with P = exp(S - lse); dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K.
+// A block holds 32 rows of one side (of a key head: K, V; of a query head: Q, dO) and walks
+// the rows of the other that its window reaches, NY at a time: both score products, then
+// the products into its own rows' sums, all register-tiled as in the forward (4 rows x NY / 16
+// scores, 4 rows x d / 16 sums a thread).  Rows lie as they are in shared memory, padded by 16
+// bytes, so the score products read four columns of a row at a time.  The key side's blocks
+// take their query rows once for each head of the group; a key tile that holds sinks is seen by
+// every later query, whose rows are cut into chunks with a partial each (launch_sink_sum).
+// Both sides in one launch: short sequences have few blocks of either.  fp32 FMAs bound it,
+// 4 d a pair on the key side and 3 d on the query side, and the length of a key block's walk
+// where there are few: 2 x 24 query and 3 key heads, 346 tokens, d = 128, window 125: 541 us
+// (the kernels of attn_block_bwd over the window's spans, four scores a thread: 1725);
+// 4 heads, 900 tokens, d = 64, window 100: 46 us (172).
+constexpr int BM = WINDOW_SIMT_ROWS;
+
+template <int D>
+constexpr int NY = D == 128 ? 32 : 64;   // (64 rows of 128 would leave one block on an SM)
+
+template <int D>
+constexpr size_t window_bwd_smem() {
+    return sizeof(float) * ((size_t)2 * BM * (D + 4) + (size_t)2 * NY<D> * (D + 4) + (size_t)2 * NY<D> * (BM + 4) + 2 * NY<D>) +
+           NY<D>;
+}
+
+template <typename T>
+__device__ __forceinline__ const T *row_of(const TensorRef &t, int b, int h, long long row) {
+    return static_cast<const T *>(t.p) + (long long)b * t.sB + (long long)h * t.sH + row * t.sT;
+}
+
+__device__ __forceinline__ void put(const BwdArgs &a, void *base, long long i, float v) {   // rounded once, if at all
+    if (a.grad_bf16)
+        static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(base)[i] = v;
+}
+
+__device__ __forceinline__ float dot4(const float4 &x, const float4 &y, float acc) {
+    return fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, fmaf(x.x, y.x, acc))));
+}
+
+template <int D, typename T, bool KEYS>
+__device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, bool vec, float *sm) {
+    constexpr int LD = D + 4, SLD = BM + 4, N = NY<D>, NJ = N / 16, NC = D / 16;
+    float *X1 = sm, *X2 = X1 + BM * LD, *Y1 = X2 + BM * LD, *Y2 = Y1 + N * LD;   // rows: K, V | Q, dO and the other side's
+    float *Ps = Y2 + N * LD, *Ss = Ps + N * SLD, *yl = Ss + N * SLD, *yd = yl + N;
+    uint8_t *hide = reinterpret_cast<uint8_t *>(yd + N);
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    // the block's rows, and the ranges of the other side's
+    const int tiles = (int)(((KEYS ? a.Lk : a.Lq) + (long long)BM - 1) / BM);
+    int tile, part = -1, bh;
+    if (KEYS) {
+        const int parts = a.n_sink_tiles * a.n_sink_parts, items = tiles - a.n_sink_tiles + parts;
+        bh = item / items;
+        tile = item % items;
+        if (tile < parts) {
+            part = tile % a.n_sink_parts;
+            tile /= a.n_sink_parts;
+        } else {
+            tile += a.n_sink_tiles - parts;
+        }
+    } else {
+        bh = item / tiles;
+        tile = tiles - 1 - item % tiles;   // the longest walks first
+    }
+    const int heads = KEYS ? a.Hkv : a.H, b = bh / heads, h = bh % heads;
+    const int r0 = tile * BM, nr = min(BM, (KEYS ? a.Lk : a.Lq) - r0);
+    long long lo[2], hi[2];
+    int spans = 1;
+    if (KEYS) {
+        lo[0] = r0 - a.q_off;
+        hi[0] = (long long)r0 + nr - 1 + a.window - a.q_off;
+        if (part >= 0) {
+            lo[0] = max(lo[0], (long long)part * a.sink_rows);
+            hi[0] = (long long)(part + 1) * a.sink_rows;
+        } else if (r0 < a.sinks) {
+            hi[0] = a.Lq;   // one chunk covers every query
+        }
+        lo[0] = max(lo[0], 0LL);
+        hi[0] = min(hi[0], (long long)a.Lq);
+    } else {
+        const long long p0 = a.q_off + r0, end = min(p0 + nr, (long long)a.Lk), first = max(0LL, p0 - a.window + 1);
+        lo[0] = 0;
+        hi[0] = end;
+        if (first > a.sinks) {   // the sinks, then the window
+            hi[0] = min((long long)a.sinks, end);
+            lo[1] = first;
+            hi[1] = end;
+            spans = 2;
+        }
+    }
+    auto hidden = [&](long long key) { return a.kpm && a.kpm[(long long)b * a.kpm_ld + key]; };
+    for (int e = t; e < BM * (D / 4); e += WT) {   // (a hidden key's rows may hold anything and are not read)
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        const bool in = r < nr && !(KEYS && hidden(r0 + r));
+        *reinterpret_cast<float4 *>(X1 + r * LD + c) = in ? load4(row_of<T>(KEYS ? a.k : a.q, b, h, r0 + r) + c, vec) : zero;
+        *reinterpret_cast<float4 *>(X2 + r * LD + c) = in ? load4(row_of<T>(KEYS ? a.v : a.dout, b, h, r0 + r) + c, vec) : zero;
+    }
+    bool in[4];
+    float xl[4], xd[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        in[i] = r < nr && !(KEYS && hidden(r0 + r));
+        xl[i] = xd[i] = 0.f;
+        if (!KEYS && in[i]) {
+            const long long at = ((long long)b * a.H + h) * a.Lq + r0 + r;
+            xl[i] = a.lse[at];
+            xd[i] = a.D[at];
+            in[i] = xl[i] != -INFINITY;
+            xl[i] *= LOG2E;
+        }
+    }
+    float acc1[4][NC], acc2[4][NC];   // dK and dV, or dQ
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            acc1[i][c] = 0.f;
+            if (KEYS) acc2[i][c] = 0.f;
+        }
+    const float sl2 = a.scale * LOG2E;
+
+    for (int step = 0; step < (KEYS ? a.kv_group : spans); ++step) {
+        const int hy = KEYS ? h * a.kv_group + step : h / a.kv_group;   // the other side's head
+        const long long y_end = hi[KEYS ? 0 : step];
+        for (long long y0 = lo[KEYS ? 0 : step]; y0 < y_end; y0 += N) {
+            const int ny = (int)min((long long)N, y_end - y0);
+            __syncthreads();   // the previous rows are read
+            if (t < N) {
+                if (KEYS) {
+                    const long long at = ((long long)b * a.H + hy) * a.Lq + y0 + t;
+                    const float l = t < ny ? a.lse[at] : -INFINITY;
+                    hide[t] = l == -INFINITY;
+                    yl[t] = l * LOG2E;
+                    yd[t] = t < ny ? a.D[at] : 0.f;
+                } else {
+                    hide[t] = t >= ny || hidden(y0 + t);
+                }
+            }
+            __syncthreads();
+            for (int e = t; e < N * (D / 4); e += WT) {
+                const int y = e / (D / 4), c = e % (D / 4) * 4;
+                const bool use = !hide[y];
+                *reinterpret_cast<float4 *>(Y1 + y * LD + c) = use ? load4(row_of<T>(KEYS ? a.q : a.k, b, hy, y0 + y) + c, vec) : zero;
+                *reinterpret_cast<float4 *>(Y2 + y * LD + c) =
+                    use ? load4(row_of<T>(KEYS ? a.dout : a.v, b, hy, y0 + y) + c, vec) : zero;
+            }
+            __syncthreads();
+            float s[4][NJ], g[4][NJ];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) s[i][j] = g[i][j] = 0.f;
+#pragma unroll 2
+            for (int c = 0; c < D; c += 4) {
+                float4 x[4], y[NJ];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(X1 + (ty * 4 + i) * LD + c);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) y[j] = *reinterpret_cast<const float4 *>(Y1 + (tx + 16 * j) * LD + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(X2 + (ty * 4 + i) * LD + c);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) y[j] = *reinterpret_cast<const float4 *>(Y2 + (tx + 16 * j) * LD + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) g[i][j] = dot4(x[i], y[j], g[i][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int y = tx + 16 * j;
+                const bool use = !hide[y];
+                const float l = KEYS ? yl[y] : 0.f, dd = KEYS ? yd[y] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const long long p = a.q_off + (KEYS ? y0 + y : (long long)r0 + ty * 4 + i);
+                    const long long key = KEYS ? (long long)r0 + ty * 4 + i : y0 + y;
+                    float pr = 0.f, ds = 0.f;
+                    if (use && in[i] && key <= p && (key > p - a.window || key < a.sinks)) {
+                        pr = exp2f(fmaf(s[i][j], sl2, -(KEYS ? l : xl[i])));
+                        ds = pr * (g[i][j] - (KEYS ? dd : xd[i]));
+                    }
+                    s[i][j] = pr;
+                    g[i][j] = ds;
+                }
+                *reinterpret_cast<float4 *>(Ss + y * SLD + ty * 4) = make_float4(g[0][j], g[1][j], g[2][j], g[3][j]);
+                if (KEYS) *reinterpret_cast<float4 *>(Ps + y * SLD + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+            }
+            __syncwarp();   // a warp's rows of P and dS are its own: 8 rows, the chunk's columns
+            auto add = [&](float(&acc)[4][NC], const float *w, const float *row) {
+                const float4 w4 = *reinterpret_cast<const float4 *>(w);
+                const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+                float v[NC];
+                if constexpr (NC >= 4) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 4) {
+                        const float4 v4 = *reinterpret_cast<const float4 *>(row + o_col<NC>(tx, c));
+                        v[c] = v4.x;
+                        v[c + 1] = v4.y;
+                        v[c + 2] = v4.z;
+                        v[c + 3] = v4.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) v[c] = row[tx * NC + c];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(wv[i], v[c], acc[i][c]);
+            };
+#pragma unroll 2
+            for (int y = 0; y < ny; ++y) {
+                add(acc1, Ss + y * SLD + ty * 4, Y1 + y * LD);
+                if constexpr (KEYS) add(acc2, Ps + y * SLD + ty * 4, Y2 + y * LD);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        if (r >= nr) continue;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = o_col<NC>(tx, c);
+            if constexpr (!KEYS) {
+                put(a, a.dq, ((long long)bh * a.Lq + r0 + r) * D + col, acc1[i][c] * a.scale);
+            } else if (part >= 0) {   // dV, then dK of the chunk's partial
+                float *dst = a.part + ((((long long)bh * a.n_sink_tiles + tile) * a.n_sink_parts + part) * 2 * BM + r) * (long long)D;
+                dst[col] = acc2[i][c];
+                dst[(long long)BM * D + col] = acc1[i][c] * a.scale;
+            } else {
+                const long long at = ((long long)bh * a.Lk + r0 + r) * D + col;
+                put(a, a.dv, at, acc2[i][c]);
+                put(a, a.dk, at, acc1[i][c] * a.scale);
+            }
+        }
+    }
+}
+
+// The key side's blocks first: their walks are the longer ones.
+template <int D, typename T>
+__global__ void __launch_bounds__(WT) window_bwd_simt_kernel(const BwdArgs a, int key_items, int vec) {
+    extern __shared__ __align__(16) float wsm[];
+    if ((int)blockIdx.x < key_items)
+        window_bwd_block<D, T, true>(a, blockIdx.x, vec, wsm);
+    else
+        window_bwd_block<D, T, false>(a, blockIdx.x - key_items, vec, wsm);
+}
+
+template <int D, typename T>
+int launch_bwd_t(const BwdArgs &a, int key_items, long long blocks, cudaStream_t s) {
+    constexpr size_t smem = window_bwd_smem<D>();
+    auto kern = window_bwd_simt_kernel<D, T>;
+    static std::atomic<unsigned long long> allowed{0};
+    if (!allow_smem(allowed, reinterpret_cast<const void *>(kern), (int)smem)) return BA_ERR_CUDA;
+    bool vec = true;
+    for (const TensorRef *t : {&a.q, &a.k, &a.v, &a.dout})
+        vec = vec && reinterpret_cast<uintptr_t>(t->p) % (4 * sizeof(T)) == 0 && t->sB % 4 == 0 && t->sH % 4 == 0 && t->sT % 4 == 0;
+    kern<<<(unsigned)blocks, WT, smem, s>>>(a, key_items, vec);
+    return cudaGetLastError() == cudaSuccess ? BA_OK : BA_ERR_CUDA;
+}
+
+template <int D>
+int launch_bwd_d(const BwdArgs &a, int key_items, long long blocks, cudaStream_t s) {
+    return a.dtype == BA_F32 ? launch_bwd_t<D, float>(a, key_items, blocks, s)
+                             : launch_bwd_t<D, __nv_bfloat16>(a, key_items, blocks, s);
+}
+
 }  // namespace
 
 int launch_window_simt(const AttnArgs &a, cudaStream_t s) {
@@ -233,6 +513,23 @@ int launch_window_simt(const AttnArgs &a, cudaStream_t s) {
         case 128: return launch_d<128>(a, blocks, s);
         default: return BA_ERR_SHAPE;
     }
+}
+
+int launch_attn_window_bwd(const BwdArgs &a, int num_sms, cudaStream_t s) {
+    int rc = launch_window_pre(a, num_sms, s);
+    if (rc) return rc;
+    const long long key_items = ((a.Lk + (long long)BM - 1) / BM - a.n_sink_tiles + (long long)a.n_sink_tiles * a.n_sink_parts) *
+                                a.B * a.Hkv;
+    const long long blocks = key_items + (a.Lq + (long long)BM - 1) / BM * a.B * a.H;
+    if (blocks > 0x7fffffffLL) return BA_ERR_SHAPE;
+    switch (a.d) {
+        case 16: rc = launch_bwd_d<16>(a, (int)key_items, blocks, s); break;
+        case 32: rc = launch_bwd_d<32>(a, (int)key_items, blocks, s); break;
+        case 64: rc = launch_bwd_d<64>(a, (int)key_items, blocks, s); break;
+        case 128: rc = launch_bwd_d<128>(a, (int)key_items, blocks, s); break;
+        default: rc = BA_ERR_SHAPE;
+    }
+    return rc ? rc : launch_sink_sum(a, BM, num_sms, s);
 }
 
 }  // namespace ba

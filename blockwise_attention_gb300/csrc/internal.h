@@ -91,6 +91,7 @@ struct BwdMaps {
 
 int launch_attn_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_bwd_pre(const BwdArgs &a, int num_sms, cudaStream_t s);
+constexpr int WINDOW_SIMT_ROWS = 32;   // rows of a block of the CUDA-core windowed backward
 int launch_attn_window_bwd(const BwdArgs &a, int num_sms, cudaStream_t s);
 int launch_attn_window_bwd_tc(const BwdArgs &a, const BwdMaps &m, int num_sms, cudaStream_t s);
 int launch_window_pre(const BwdArgs &a, int num_sms, cudaStream_t s);
