@@ -4,11 +4,14 @@
 // O_i = sum_j p_ij v_j / l_i with the running (max, l, O) of an online softmax; see
 // attn_window_fwd for the visible pairs.  What bounds it is the fp32 FMA rate: 2 d FMAs a
 // pair.  A block of 128 threads takes 32 queries of one head and walks their keys (the
-// sinks, then the window) 64 at a time; both products are register-tiled, 4 x 4 scores and
-// 4 rows x d / 16 columns of O a thread, with the contracted index leading in shared
-// memory (Q and K transposed, P transposed, V as it is), so that a step reads two (or
+// sinks and the window as one range) 64 at a time; both products are register-tiled, 4 x 4
+// scores and 4 rows x d / 16 columns of O a thread, with the contracted index leading in
+// shared memory (Q and K transposed, P transposed, V as it is), so that a step reads two (or
 // three) 16-byte words for 16 (or 4 d / 16) FMAs.  32 rows a block rather than 64: a
 // chunk of a prompt has few tiles, and twice the blocks fill the SMs more evenly.
+// 2 x 765 queries behind 259, 8 heads of 64, window 257: 55 us (a thread a row: 258; the sinks
+// as a tile of their own and K read a row a lane: 59), 32 % of the FMA rate: 2.5 blocks of four
+// warps an SM hide little of what they wait for in shared memory and L2.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -41,6 +44,16 @@ __device__ __forceinline__ int o_col(int tx, int c) {
     return N == 8 ? (c < 4 ? tx * 4 + c : 64 + tx * 4 + c - 4) : tx * N + c;
 }
 
+// Row and column of a thread's four values when R rows are read and stored transposed: a warp
+// takes 8 rows of 64 bytes (fp32), 16 lines instead of the 32 of a row a lane, and its
+// stores meet two to a bank.
+template <int R>
+__device__ __forceinline__ void transposed_place(int e, int &row, int &col) {
+    const int lane = e & 31, w = e >> 5;
+    row = w % (R / 8) * 8 + (lane & 7);
+    col = (w / (R / 8) * 4 + (lane >> 3)) * 4;
+}
+
 template <int D>
 constexpr size_t window_simt_smem() {
     return sizeof(float) * ((size_t)D * QLD + (size_t)D * KLD + (size_t)WN * D + (size_t)WN * QLD) + WN;
@@ -64,7 +77,8 @@ __global__ void __launch_bounds__(WT) window_simt_kernel(const AttnArgs a, int v
     const T *vb = static_cast<const T *>(a.v) + (long long)b * a.vsB + (long long)hk * a.vsH;
 
     for (int e = t; e < WM * (D / 4); e += WT) {
-        const int r = e % WM, c = e / WM * 4;
+        int r, c;
+        transposed_place<WM>(e, r, c);
         const float4 x = r < nr ? load4(qb + (long long)(r0 + r) * a.qsT + c, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
         Qt[c * QLD + r] = x.x;
         Qt[(c + 1) * QLD + r] = x.y;
@@ -82,100 +96,103 @@ __global__ void __launch_bounds__(WT) window_simt_kernel(const AttnArgs a, int v
     const long long p_last = p0 + nr - 1;
     const int end = (int)min(p_last + 1, (long long)g.Lk);
     const int lo = (int)max(0LL, p0 - g.window + 1), first = lo > g.sinks ? min(g.sinks, end) : 0;
-    // chunk 0: the sinks [0, first); chunk 1: the window's keys
-    for (int chunk = first > 0 ? 0 : 1; chunk < 2; ++chunk) {
-        const int c0 = chunk == 0 ? 0 : (lo > g.sinks ? lo : 0), c1 = chunk == 0 ? first : end;
-        for (int j0 = c0; j0 < c1; j0 += WN) {
-            const int nk = min(WN, c1 - j0);
-            __syncthreads();   // the previous tile is read
-            if (t < WN) hide[t] = t >= nk || (g.kpm && g.kpm[(long long)b * g.kpm_ld + j0 + t]);
-            __syncthreads();
-            // (hidden keys are not read: what they hold has no effect)
-            for (int e = t; e < WN * (D / 4); e += WT) {
-                const int j = e % WN, c = e / WN * 4;
-                const float4 x = hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(kb + (long long)(j0 + j) * a.ksT + c, vec);
-                Kt[c * KLD + j] = x.x;
-                Kt[(c + 1) * KLD + j] = x.y;
-                Kt[(c + 2) * KLD + j] = x.z;
-                Kt[(c + 3) * KLD + j] = x.w;
-            }
-            for (int e = t; e < WN * (D / 4); e += WT) {
-                const int j = e / (D / 4), c = e % (D / 4) * 4;
-                *reinterpret_cast<float4 *>(Vs + j * D + c) =
-                    hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(vb + (long long)(j0 + j) * a.vsT + c, vec);
-            }
-            __syncthreads();
-            float s[4][4];
+    // The keys that the rows see as one range without a gap: the sinks before the window, then its keys.
+    const int shift = lo > g.sinks ? lo - first : 0, n = lo > g.sinks ? first + max(0, end - lo) : end;
+    auto key_at = [&](int i) { return i < first ? i : i + shift; };
+    for (int j0 = 0; j0 < n; j0 += WN) {
+        const int nk = min(WN, n - j0);
+        __syncthreads();   // the previous tile is read
+        if (t < WN) hide[t] = t >= nk || (g.kpm && g.kpm[(long long)b * g.kpm_ld + key_at(j0 + t)]);
+        __syncthreads();
+        // (hidden keys are not read: what they hold has no effect)
+        for (int e = t; e < WN * (D / 4); e += WT) {
+            int j, c;
+            transposed_place<WN>(e, j, c);
+            const float4 x = hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(kb + (long long)key_at(j0 + j) * a.ksT + c, vec);
+            Kt[c * KLD + j] = x.x;
+            Kt[(c + 1) * KLD + j] = x.y;
+            Kt[(c + 2) * KLD + j] = x.z;
+            Kt[(c + 3) * KLD + j] = x.w;
+        }
+        for (int e = t; e < WN * (D / 4); e += WT) {
+            const int j = e / (D / 4), c = e % (D / 4) * 4;
+            *reinterpret_cast<float4 *>(Vs + j * D + c) =
+                hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(vb + (long long)key_at(j0 + j) * a.vsT + c, vec);
+        }
+        __syncthreads();
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 8
+        for (int c = 0; c < D; ++c) {
+            const float4 q4 = *reinterpret_cast<const float4 *>(Qt + c * QLD + ty * 4);
+            const float4 k4 = *reinterpret_cast<const float4 *>(Kt + c * KLD + tx * 4);
+            const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+                for (int j = 0; j < 4; ++j) s[i][j] = fmaf(qv[i], kv[j], s[i][j]);
+        }
+        // every pair of the tile visible: the last key before the first row, the first
+        // one inside the last row's window (or all of them sinks), none hidden
+        const int k_lo = key_at(j0), k_hi = key_at(j0 + WN - 1);
+        const bool whole = nk == WN && k_hi <= p0 && (k_lo > p_last - g.window || k_hi < g.sinks) && !g.kpm;
+        const int hid = *reinterpret_cast<const int *>(hide + tx * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long p = p0 + ty * 4 + i;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = key_at(j0 + tx * 4 + j);
+                s[i][j] *= a.scale_log2;
+                if (!whole && ((hid >> (8 * j) & 0xff) || key > p || (key <= p - g.window && key >= g.sinks)))
+                    s[i][j] = -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off, 16));
+            const float m_new = fmaxf(m[i], mx), base = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = exp2f(m[i] - base);   // 0 before the first key
+            m[i] = m_new;
+            l[i] *= alpha;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(s[i][j] - base);
+                l[i] += s[i][j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4 *>(Pt + (tx * 4 + j) * QLD + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+        __syncwarp();   // a warp's rows of P are its own: 8 rows, all keys
+        const int nk8 = (nk + 7) / 8 * 8;   // (P and V are zero behind nk)
 #pragma unroll 8
-            for (int c = 0; c < D; ++c) {
-                const float4 q4 = *reinterpret_cast<const float4 *>(Qt + c * QLD + ty * 4);
-                const float4 k4 = *reinterpret_cast<const float4 *>(Kt + c * KLD + tx * 4);
-                const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int j = 0; j < nk8; ++j) {
+            const float4 p4 = *reinterpret_cast<const float4 *>(Pt + j * QLD + ty * 4);
+            const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
+            float vv[NC];
+            if constexpr (NC >= 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][j] = fmaf(qv[i], kv[j], s[i][j]);
-            }
-            // every pair of the tile visible: the last key before the first row, the first
-            // one inside the last row's window (or all of them sinks), none hidden
-            const bool whole = nk == WN && j0 + WN - 1 <= p0 && (j0 > p_last - g.window || j0 + WN <= g.sinks) && !g.kpm;
-            const int hid = *reinterpret_cast<const int *>(hide + tx * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long long p = p0 + ty * 4 + i;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = j0 + tx * 4 + j;
-                    s[i][j] *= a.scale_log2;
-                    if (!whole && ((hid >> (8 * j) & 0xff) || key > p || (key <= p - g.window && key >= g.sinks)))
-                        s[i][j] = -INFINITY;
-                    mx = fmaxf(mx, s[i][j]);
+                for (int c = 0; c < NC; c += 4) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(Vs + j * D + o_col<NC>(tx, c));
+                    vv[c] = v4.x;
+                    vv[c + 1] = v4.y;
+                    vv[c + 2] = v4.z;
+                    vv[c + 3] = v4.w;
                 }
+            } else {
 #pragma unroll
-                for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off, 16));
-                const float m_new = fmaxf(m[i], mx), base = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = exp2f(m[i] - base);   // 0 before the first key
-                m[i] = m_new;
-                l[i] *= alpha;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) o[i][c] *= alpha;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = exp2f(s[i][j] - base);
-                    l[i] += s[i][j];
-                }
+                for (int c = 0; c < NC; ++c) vv[c] = Vs[j * D + tx * NC + c];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4 *>(Pt + (tx * 4 + j) * QLD + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-            __syncwarp();   // a warp's rows of P are its own: 8 rows, all keys
-            for (int j = 0; j < nk; ++j) {
-                const float4 p4 = *reinterpret_cast<const float4 *>(Pt + j * QLD + ty * 4);
-                const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
-                float vv[NC];
-                if constexpr (NC >= 4) {
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < NC; c += 4) {
-                        const float4 v4 = *reinterpret_cast<const float4 *>(Vs + j * D + o_col<NC>(tx, c));
-                        vv[c] = v4.x;
-                        vv[c + 1] = v4.y;
-                        vv[c + 2] = v4.z;
-                        vv[c + 3] = v4.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) vv[c] = Vs[j * D + tx * NC + c];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) o[i][c] = fmaf(pv[i], vv[c], o[i][c]);
-            }
+                for (int c = 0; c < NC; ++c) o[i][c] = fmaf(pv[i], vv[c], o[i][c]);
         }
     }
 #pragma unroll
@@ -292,30 +309,30 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
     }
     const int heads = KEYS ? a.Hkv : a.H, b = bh / heads, h = bh % heads;
     const int r0 = tile * BM, nr = min(BM, (KEYS ? a.Lk : a.Lq) - r0);
-    long long lo[2], hi[2];
-    int spans = 1;
+    // (query side: the keys as one range without a gap, as in the forward)
+    long long lo = 0, hi, first = 0, shift = 0;
     if (KEYS) {
-        lo[0] = r0 - a.q_off;
-        hi[0] = (long long)r0 + nr - 1 + a.window - a.q_off;
+        lo = r0 - a.q_off;
+        hi = (long long)r0 + nr - 1 + a.window - a.q_off;
         if (part >= 0) {
-            lo[0] = max(lo[0], (long long)part * a.sink_rows);
-            hi[0] = (long long)(part + 1) * a.sink_rows;
+            lo = max(lo, (long long)part * a.sink_rows);
+            hi = (long long)(part + 1) * a.sink_rows;
         } else if (r0 < a.sinks) {
-            hi[0] = a.Lq;   // one chunk covers every query
+            hi = a.Lq;   // one chunk covers every query
         }
-        lo[0] = max(lo[0], 0LL);
-        hi[0] = min(hi[0], (long long)a.Lq);
+        lo = max(lo, 0LL);
+        hi = min(hi, (long long)a.Lq);
     } else {
-        const long long p0 = a.q_off + r0, end = min(p0 + nr, (long long)a.Lk), first = max(0LL, p0 - a.window + 1);
-        lo[0] = 0;
-        hi[0] = end;
-        if (first > a.sinks) {   // the sinks, then the window
-            hi[0] = min((long long)a.sinks, end);
-            lo[1] = first;
-            hi[1] = end;
-            spans = 2;
+        const long long p0 = a.q_off + r0, end = min(p0 + nr, (long long)a.Lk), from = max(0LL, p0 - a.window + 1);
+        if (from > a.sinks) {
+            first = min((long long)a.sinks, end);
+            shift = from - first;
+            hi = first + max(0LL, end - from);
+        } else {
+            hi = end;
         }
     }
+    auto at = [&](long long y) { return KEYS || y < first ? y : y + shift; };
     auto hidden = [&](long long key) { return a.kpm && a.kpm[(long long)b * a.kpm_ld + key]; };
     for (int e = t; e < BM * (D / 4); e += WT) {   // (a hidden key's rows may hold anything and are not read)
         const int r = e / (D / 4), c = e % (D / 4) * 4;
@@ -331,9 +348,9 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
         in[i] = r < nr && !(KEYS && hidden(r0 + r));
         xl[i] = xd[i] = 0.f;
         if (!KEYS && in[i]) {
-            const long long at = ((long long)b * a.H + h) * a.Lq + r0 + r;
-            xl[i] = a.lse[at];
-            xd[i] = a.D[at];
+            const long long row = ((long long)b * a.H + h) * a.Lq + r0 + r;
+            xl[i] = a.lse[row];
+            xd[i] = a.D[row];
             in[i] = xl[i] != -INFINITY;
             xl[i] *= LOG2E;
         }
@@ -348,30 +365,29 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
         }
     const float sl2 = a.scale * LOG2E;
 
-    for (int step = 0; step < (KEYS ? a.kv_group : spans); ++step) {
+    for (int step = 0; step < (KEYS ? a.kv_group : 1); ++step) {
         const int hy = KEYS ? h * a.kv_group + step : h / a.kv_group;   // the other side's head
-        const long long y_end = hi[KEYS ? 0 : step];
-        for (long long y0 = lo[KEYS ? 0 : step]; y0 < y_end; y0 += N) {
-            const int ny = (int)min((long long)N, y_end - y0);
+        for (long long y0 = lo; y0 < hi; y0 += N) {
+            const int ny = (int)min((long long)N, hi - y0);
             __syncthreads();   // the previous rows are read
             if (t < N) {
                 if (KEYS) {
-                    const long long at = ((long long)b * a.H + hy) * a.Lq + y0 + t;
-                    const float l = t < ny ? a.lse[at] : -INFINITY;
+                    const long long row = ((long long)b * a.H + hy) * a.Lq + y0 + t;
+                    const float l = t < ny ? a.lse[row] : -INFINITY;
                     hide[t] = l == -INFINITY;
                     yl[t] = l * LOG2E;
-                    yd[t] = t < ny ? a.D[at] : 0.f;
+                    yd[t] = t < ny ? a.D[row] : 0.f;
                 } else {
-                    hide[t] = t >= ny || hidden(y0 + t);
+                    hide[t] = t >= ny || hidden(at(y0 + t));
                 }
             }
             __syncthreads();
             for (int e = t; e < N * (D / 4); e += WT) {
                 const int y = e / (D / 4), c = e % (D / 4) * 4;
                 const bool use = !hide[y];
-                *reinterpret_cast<float4 *>(Y1 + y * LD + c) = use ? load4(row_of<T>(KEYS ? a.q : a.k, b, hy, y0 + y) + c, vec) : zero;
+                *reinterpret_cast<float4 *>(Y1 + y * LD + c) = use ? load4(row_of<T>(KEYS ? a.q : a.k, b, hy, at(y0 + y)) + c, vec) : zero;
                 *reinterpret_cast<float4 *>(Y2 + y * LD + c) =
-                    use ? load4(row_of<T>(KEYS ? a.dout : a.v, b, hy, y0 + y) + c, vec) : zero;
+                    use ? load4(row_of<T>(KEYS ? a.dout : a.v, b, hy, at(y0 + y)) + c, vec) : zero;
             }
             __syncthreads();
             float s[4][NJ], g[4][NJ];
@@ -407,7 +423,7 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const long long p = a.q_off + (KEYS ? y0 + y : (long long)r0 + ty * 4 + i);
-                    const long long key = KEYS ? (long long)r0 + ty * 4 + i : y0 + y;
+                    const long long key = KEYS ? (long long)r0 + ty * 4 + i : at(y0 + y);
                     float pr = 0.f, ds = 0.f;
                     if (use && in[i] && key <= p && (key > p - a.window || key < a.sinks)) {
                         pr = exp2f(fmaf(s[i][j], sl2, -(KEYS ? l : xl[i])));
@@ -442,8 +458,9 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
 #pragma unroll
                     for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(wv[i], v[c], acc[i][c]);
             };
-#pragma unroll 2
-            for (int y = 0; y < ny; ++y) {
+            const int ny4 = (ny + 3) / 4 * 4;   // (dS, P and the rows are zero behind ny)
+#pragma unroll 4
+            for (int y = 0; y < ny4; ++y) {
                 add(acc1, Ss + y * SLD + ty * 4, Y1 + y * LD);
                 if constexpr (KEYS) add(acc2, Ps + y * SLD + ty * 4, Y2 + y * LD);
             }
@@ -463,9 +480,9 @@ __device__ __forceinline__ void window_bwd_block(const BwdArgs &a, int item, boo
                 dst[col] = acc2[i][c];
                 dst[(long long)BM * D + col] = acc1[i][c] * a.scale;
             } else {
-                const long long at = ((long long)bh * a.Lk + r0 + r) * D + col;
-                put(a, a.dv, at, acc2[i][c]);
-                put(a, a.dk, at, acc1[i][c] * a.scale);
+                const long long to = ((long long)bh * a.Lk + r0 + r) * D + col;
+                put(a, a.dv, to, acc2[i][c]);
+                put(a, a.dk, to, acc1[i][c] * a.scale);
             }
         }
     }

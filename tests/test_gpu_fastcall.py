@@ -155,3 +155,56 @@ def test_dtypes_and_whole_floats_go_the_python_way():
         ba.attn_window_decode_fwd(q.half(), k.half(), k.half(), window=8)
     a, b = ba.attn_window_decode_fwd(q, k, k, window=8.0, scale=1), ba.attn_window_decode_fwd(q, k, k, window=8, scale=1.0)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_threads_on_streams_of_their_own():
+    """Host threads that call at once, each on its stream and with its own sizes and rotation base."""
+    import threading
+    n, want, got = 4, [], [None] * 4
+    args = [(rnd(2, 4, 1, 64, seed=i), rnd(2, 2, 100 + 50 * i, 64, seed=i), rnd(64, dtype=torch.float32, seed=i)) for i in range(n)]
+
+    def work(q, k, w, i):
+        y, _ = ba.qk_norm_rope_fwd(q, k[:, :, :1], w, w, base=1000.0 * (i + 1))
+        out, lse = ba.attn_window_decode_fwd(y, k, k, window=30 + i)
+        c = ba.kv4_append(ba.KV4Cache.empty(2, 2, 64, 64), k[:, :, :64], k[:, :, :64])
+        return out, lse, *ba.attn_decode_kv4_fwd(y, c)
+
+    for i, a in enumerate(args):
+        want.append(work(*a, i))
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got[i] = work(*args[i], i)
+        s.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(n)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for w, g in zip(want, got):
+        assert g is not None and all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+class Windowed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v):
+        out, lse = ba.attn_window_fwd(q, k, v, window=20, sinks=1)
+        ctx.save_for_backward(q, k, v, out, lse)
+        return out
+
+    @staticmethod
+    def backward(ctx, g):
+        q, k, v, out, lse = ctx.saved_tensors
+        return ba.attn_window_bwd(q, k, v, out, g.contiguous(), lse, window=20, sinks=1)
+
+
+def test_parameters_autograd_and_inference_mode():
+    q, k, v = (torch.nn.Parameter(rnd(1, H, 60, 64, dtype=torch.float32, seed=H)) for H in (4, 2, 2))
+    Windowed.apply(q, k, v).square().sum().backward()
+    out, lse = ba.attn_window_fwd(q.detach(), k.detach(), v.detach(), window=20, sinks=1)
+    want = ba.attn_window_bwd(q.detach(), k.detach(), v.detach(), out, 2 * out, lse, window=20, sinks=1)
+    assert all(torch.equal(a.grad, b) for a, b in zip((q, k, v), want))
+    with torch.inference_mode():
+        o2, l2 = ba.attn_window_fwd(q, k, v, window=20, sinks=1)
+        assert o2.is_inference() and torch.equal(o2, out) and torch.equal(l2, lse)
