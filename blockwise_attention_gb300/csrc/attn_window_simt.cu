@@ -9,9 +9,10 @@
 // shared memory (Q and K transposed, P transposed, V as it is), so that a step reads two (or
 // three) 16-byte words for 16 (or 4 d / 16) FMAs.  32 rows a block rather than 64: a
 // chunk of a prompt has few tiles, and twice the blocks fill the SMs more evenly.
-// 2 x 765 queries behind 259, 8 heads of 64, window 257: 55 us (a thread a row: 258; the sinks
-// as a tile of their own and K read a row a lane: 59), 32 % of the FMA rate: 2.5 blocks of four
-// warps an SM hide little of what they wait for in shared memory and L2.
+// 2 x 765 queries behind 259, 8 heads of 64, window 257: 47.5 us (a thread a row: 258; the
+// sinks as a tile of their own and K read a row a lane: 59; K and V loaded where they are
+// needed instead of ahead: 55).  2.5 blocks of four warps an SM hide little of the rest of
+// what they wait for in shared memory.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -56,7 +57,7 @@ __device__ __forceinline__ void transposed_place(int e, int &row, int &col) {
 
 template <int D>
 constexpr size_t window_simt_smem() {
-    return sizeof(float) * ((size_t)D * QLD + (size_t)D * KLD + (size_t)WN * D + (size_t)WN * QLD) + WN;
+    return sizeof(float) * ((size_t)D * QLD + (size_t)D * KLD + (size_t)WN * D + (size_t)WN * QLD) + 2 * WN;
 }
 
 template <int D, typename T>
@@ -99,27 +100,53 @@ __global__ void __launch_bounds__(WT) window_simt_kernel(const AttnArgs a, int v
     // The keys that the rows see as one range without a gap: the sinks before the window, then its keys.
     const int shift = lo > g.sinks ? lo - first : 0, n = lo > g.sinks ? first + max(0, end - lo) : end;
     auto key_at = [&](int i) { return i < first ? i : i + shift; };
+    // The next tile's K is loaded into registers while this one is worked on, V (fp32) by
+    // cp.async while the scores are formed.  Hidden keys are not read: what they hold has no effect.
+    constexpr int KN = D * WN / 4 / WT;
+    const bool async = sizeof(T) == 4 && vec;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 next[KN];
+    auto mark = [&](int j0, uint8_t *hd) {
+        if (t < WN) hd[t] = j0 + t >= n || (g.kpm && g.kpm[(long long)b * g.kpm_ld + key_at(j0 + t)]);
+    };
+    auto fetch = [&](int j0, const uint8_t *hd) {
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            int j, c;
+            transposed_place<WN>(t + i * WT, j, c);
+            next[i] = hd[j] ? zero : load4(kb + (long long)key_at(j0 + j) * a.ksT + c, vec);
+        }
+    };
+    mark(0, hide);
+    __syncthreads();
+    fetch(0, hide);
     for (int j0 = 0; j0 < n; j0 += WN) {
         const int nk = min(WN, n - j0);
+        uint8_t *hd = hide + (j0 / WN & 1) * WN, *hd_next = hide + (~(j0 / WN) & 1) * WN;
         __syncthreads();   // the previous tile is read
-        if (t < WN) hide[t] = t >= nk || (g.kpm && g.kpm[(long long)b * g.kpm_ld + key_at(j0 + t)]);
-        __syncthreads();
-        // (hidden keys are not read: what they hold has no effect)
-        for (int e = t; e < WN * (D / 4); e += WT) {
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
             int j, c;
-            transposed_place<WN>(e, j, c);
-            const float4 x = hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(kb + (long long)key_at(j0 + j) * a.ksT + c, vec);
-            Kt[c * KLD + j] = x.x;
-            Kt[(c + 1) * KLD + j] = x.y;
-            Kt[(c + 2) * KLD + j] = x.z;
-            Kt[(c + 3) * KLD + j] = x.w;
+            transposed_place<WN>(t + i * WT, j, c);
+            Kt[c * KLD + j] = next[i].x;
+            Kt[(c + 1) * KLD + j] = next[i].y;
+            Kt[(c + 2) * KLD + j] = next[i].z;
+            Kt[(c + 3) * KLD + j] = next[i].w;
         }
         for (int e = t; e < WN * (D / 4); e += WT) {
             const int j = e / (D / 4), c = e % (D / 4) * 4;
-            *reinterpret_cast<float4 *>(Vs + j * D + c) =
-                hide[j] ? make_float4(0.f, 0.f, 0.f, 0.f) : load4(vb + (long long)key_at(j0 + j) * a.vsT + c, vec);
+            const T *from = vb + (long long)(hd[j] ? 0 : key_at(j0 + j)) * a.vsT + c;
+            if (async)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(Vs + j * D + c)),
+                             "l"(from), "r"(hd[j] ? 0 : 16)
+                             : "memory");
+            else
+                *reinterpret_cast<float4 *>(Vs + j * D + c) = hd[j] ? zero : load4(from, vec);
         }
+        if (j0 + WN < n) mark(j0 + WN, hd_next);
         __syncthreads();
+        if (j0 + WN < n) fetch(j0 + WN, hd_next);
         float s[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -139,7 +166,7 @@ __global__ void __launch_bounds__(WT) window_simt_kernel(const AttnArgs a, int v
         // one inside the last row's window (or all of them sinks), none hidden
         const int k_lo = key_at(j0), k_hi = key_at(j0 + WN - 1);
         const bool whole = nk == WN && k_hi <= p0 && (k_lo > p_last - g.window || k_hi < g.sinks) && !g.kpm;
-        const int hid = *reinterpret_cast<const int *>(hide + tx * 4);
+        const int hid = *reinterpret_cast<const int *>(hd + tx * 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const long long p = p0 + ty * 4 + i;
@@ -169,7 +196,12 @@ __global__ void __launch_bounds__(WT) window_simt_kernel(const AttnArgs a, int v
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<float4 *>(Pt + (tx * 4 + j) * QLD + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-        __syncwarp();   // a warp's rows of P are its own: 8 rows, all keys
+        if (async) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();   // V
+        } else {
+            __syncwarp();   // a warp's rows of P are its own: 8 rows, all keys
+        }
         const int nk8 = (nk + 7) / 8 * 8;   // (P and V are zero behind nk)
 #pragma unroll 8
         for (int j = 0; j < nk8; ++j) {
