@@ -14,6 +14,7 @@ import importlib.util
 import os
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 import torch
@@ -39,7 +40,7 @@ MODES = {"stepwise": 0, "fused": 1}
 BA_TILE_EMPTY, BA_TILE_FULL, BA_TILE_PARTIAL = 0, 1, 2
 
 _lib = None
-_fast = None   # the module of csrc/fastcall.cpp, where the interpreter's headers are installed
+_fast = None   # the module of csrc/fastcall.cpp, where it could be built
 
 
 class BlockAttnError(RuntimeError):
@@ -66,16 +67,18 @@ def _stale() -> bool:
 
 
 def _build_fastcall(force):
-    """Compile csrc/fastcall.cpp against torch, where the interpreter's headers are installed."""
+    """Compile csrc/fastcall.cpp against torch, where the headers of both are installed.  A torch whose
+    C++ interface differs is warned of: every call then goes through the Python binding."""
     src, header = os.path.join(_CSRC, "fastcall.cpp"), os.path.join(_ROOT, "include", "blockattn.h")
     python = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(python, "Python.h")):
+    torch_dir = os.path.dirname(torch.__file__)
+    torch_header = os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h")
+    if not (os.path.exists(os.path.join(python, "Python.h")) and os.path.exists(torch_header)):
         return
     if not force and os.path.exists(FASTCALL_PATH) and \
             os.path.getmtime(FASTCALL_PATH) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return
     os.makedirs(_BUILD, exist_ok=True)
-    torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [os.path.join(_ROOT, "include"), python, os.path.join(torch_dir, "include"), cuda]
     libs = os.path.join(torch_dir, "lib")
@@ -85,7 +88,10 @@ def _build_fastcall(force):
            f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{src} did not compile:\n{r.stderr}")
+        if os.path.exists(FASTCALL_PATH):   # of other sources
+            os.remove(FASTCALL_PATH)
+        warnings.warn(f"{src} did not compile, calls are marshalled in Python:\n{r.stderr}")
+        return
     os.replace(tmp, FASTCALL_PATH)
 
 

@@ -102,7 +102,7 @@ class Counted:
 def test_same_bits_both_ways(call, dtype, monkeypatch):
     _lib.load()
     if _lib._fast is None:
-        pytest.skip("the interpreter's headers are not installed")
+        pytest.skip("the call marshalling could not be built")
     counted = Counted(_lib._fast)
     monkeypatch.setattr(_lib, "_fast", counted)
     fast = call(dtype)
