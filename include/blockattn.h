@@ -322,7 +322,8 @@ int attn_window_fwd(ba_tensor q, ba_tensor k, ba_tensor v,
  *    the forward.  q, out and dout hold finite values.
  *  dq: (B, Hq, Lq, d); dk, dv: (B, Hkv, Lk, d), contiguous, overwritten, grad_dtype
  *    = BA_F32 or dtype (sums in fp32, rounded once; on the tensor cores P and dS are
- *    rounded to bf16 for their products).
+ *    rounded to bf16 for their products).  D_i = dout_i . out_i is formed from out as it
+ *    is given, in fp32 sums.
  *  workspace: attn_window_bwd_workspace_size() bytes: D_i per row, and for the key
  *    tiles that hold sinks (seen by every later query) fp32 partials over chunks of
  *    the queries, added in a fixed order.  No atomics: equal calls give equal bits.
